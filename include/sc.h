@@ -447,6 +447,146 @@ int sc_matmul_static_ws(const sc_matmul_desc *desc, const uint8_t *a_lv, const f
  * Returns the count, or minus an SC_ERR_* status as sc_matmul_engine. */
 int sc_matmul_launches(const sc_matmul_desc *desc, const sc_table *table);
 
+/* ---- floating-point layers of a transformer block --------------------------
+ * The layer norms in front of the SC linears, and the linear layers that a
+ * schedule leaves in floating point ("scmp_vit" README, the skip_worst
+ * schedules), each with its backward pass.  The conventions at the top of this
+ * file hold; matrices are row-major with a row stride ("ld", in elements) and
+ * only the [rows x cols] part of a matrix is written, never its padding. */
+
+/* element types */
+#define SC_F32 0
+#define SC_BF16 1
+#define SC_F16 2
+
+/* activations of sc_linear */
+#define SC_ACT_NONE 0
+#define SC_ACT_RELU 1
+#define SC_ACT_GELU 2       /* z Phi(z), the erf form                              */
+#define SC_ACT_GELU_TANH 3  /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))        */
+#define SC_ACT_SILU 4       /* z / (1 + exp(-z))                                   */
+
+/* Problem description of the layer norm and its backward pass.  x_type is the
+ * type of x, dx and dx_add, y_type that of y and dy, w_type that of weight, bias
+ * and their gradients; x_type and y_type may differ where one of them is
+ * SC_F32.  A row stride that belongs to no pointer of the call is ignored. */
+typedef struct sc_norm_desc {
+    int64_t rows, cols;    /* 0 <= rows < 2^31, 1 <= cols < 2^31               */
+    int64_t ld_x;          /* >= cols, elements between rows of x              */
+    int64_t ld_y;          /* the same for y (or dy)                           */
+    int64_t ld_dx;         /* the same for dx                                  */
+    int64_t ld_add;        /* the same for dx_add                              */
+    double eps;            /* >= 0, finite (forward only)                      */
+    int32_t x_type, y_type, w_type; /* SC_F32, SC_BF16 or SC_F16               */
+    void *workspace;       /* (device, 256-byte aligned) scratch of the backward
+                            * pass when it returns weight or bias gradients, at
+                            * least sc_layer_norm_workspace_bytes; contents on
+                            * return are unspecified; calls that may overlap
+                            * must not share one                               */
+    int64_t workspace_bytes;
+} sc_norm_desc;
+
+/* sc_layer_norm -- layer norm over the last axis.  For every row
+ *     mu = mean_j x_j,   r = 1 / sqrt(mean_j (x_j - mu)^2 + eps),
+ *     y_j = (x_j - mu) r weight_j + bias_j
+ * with every sum in fp32 (the variance about the mean, in a second pass over
+ * the row on chip) and one rounding to y_type.
+ *   weight, bias  (device, nullable: 1 and 0) [cols]
+ *   y             (device) out; may be x itself (same type and stride)
+ *   mean, rstd    (device, nullable) fp32 [rows] out: mu and r, for the backward
+ * A row that holds a NaN or an infinity gives NaN, other rows are unaffected;
+ * with eps = 0 so does a constant row.  Errors: SC_ERR_ARG, SC_ERR_UNSUPPORTED
+ * (a pair of 16-bit types that differ), SC_ERR_CUDA. */
+int sc_layer_norm(const sc_norm_desc *desc, const void *x, const void *weight, const void *bias,
+                  void *y, float *mean, float *rstd, void *stream);
+
+/* sc_layer_norm_backward -- gradients of sc_layer_norm.  With h = (x - mu) r and
+ * g = dy weight:
+ *     dx = r (g - mean_j g - h mean_j (g h)) [+ dx_add]
+ *     dweight_j = sum_i dy_ij h_ij,   dbias_j = sum_i dy_ij
+ * Sums are fp32, in an order that depends on the sizes, the alignment and the
+ * device alone (no atomics): the same call gives the same bits.
+ *   mean, rstd       (device) fp32 [rows], from the forward pass
+ *   dx_add           (device, nullable) added to dx before its one rounding (the
+ *                    gradient that reaches x past the norm, on the residual path)
+ *   dx               (device, nullable) out; may be dx_add itself (same stride)
+ *   dweight, dbias   (device, nullable) out, overwritten [cols]; with rows == 0
+ *                    they are zeroed
+ * Errors: SC_ERR_ARG (a workspace that is too small among them),
+ *         SC_ERR_UNSUPPORTED, SC_ERR_CUDA. */
+int sc_layer_norm_backward(const sc_norm_desc *desc, const void *dy, const void *x,
+                           const void *weight, const float *mean, const float *rstd,
+                           const void *dx_add, void *dx, void *dweight, void *dbias, void *stream);
+
+/* Workspace bytes of sc_layer_norm_backward when it returns dweight or dbias,
+ * for these rows, cols and types, whatever the strides and pointers; or minus an
+ * SC_ERR_* status.  Host only. */
+int64_t sc_layer_norm_workspace_bytes(const sc_norm_desc *desc);
+
+/* Problem description of the linear layer and its backward pass.
+ *   type       of x, w, pre and dx
+ *   out_type   of out, residual and dout: type or SC_F32
+ *   bias_type  of bias: any
+ *   grad_type  of dw and dbias: any (type is what an optimiser in type wants)
+ * A stride or type that belongs to no pointer of the call is ignored. */
+typedef struct sc_linear_desc {
+    int64_t M, N, K;   /* 0 <= M, N and 1 <= K, each < 2^31                    */
+    int64_t ld_x;      /* >= K: x [M][K]                                       */
+    int64_t ld_w;      /* >= K: w [N][K]                                       */
+    int64_t ld_out;    /* >= N: out or dout [M][N]                             */
+    int64_t ld_res;    /* >= N: residual [M][N]                                */
+    int64_t ld_pre;    /* >= N: pre [M][N]                                     */
+    int64_t ld_dx;     /* >= K: dx [M][K]                                      */
+    int64_t ld_dw;     /* >= K: dw [N][K]                                      */
+    int32_t type, out_type, bias_type, grad_type;
+    int32_t act;       /* SC_ACT_*                                             */
+    void *workspace;   /* (device, 256-byte aligned) scratch, at least what the
+                        * workspace queries below return (NULL where that is 0);
+                        * contents on return are unspecified; calls that may
+                        * overlap must not share one                           */
+    int64_t workspace_bytes;
+} sc_linear_desc;
+
+/* sc_linear -- one matrix product with its epilogue:
+ *     z = x w^T + bias,   out = act(z) + residual
+ * Products of 16-bit operands are exact and summed in fp32 on the tensor cores;
+ * fp32 operands are split into three bf16 parts each (exactly: 3 x 8 bits of
+ * significand) whose six leading products are summed in fp32.  bias, act and
+ * residual are applied in fp32 and out is rounded once.
+ *   bias       (device, nullable) [N]
+ *   residual   (device, nullable) [M][N] of out_type
+ *   out        (device) out; may be residual itself (same stride)
+ *   pre        (device, nullable) out: z rounded to type, for the backward pass
+ *   dev_status (device, nullable) receives SC_DEV_WAIT_LIMIT if an internal
+ *              bounded wait gave up (outputs are then unspecified)
+ * Non-finite operands give non-finite results in the rows and columns they
+ * reach (with fp32 operands an infinity may come out as a NaN).
+ * Errors: SC_ERR_ARG (a workspace that is too small among them), SC_ERR_CUDA. */
+int sc_linear(const sc_linear_desc *desc, const void *x, const void *w, const void *bias,
+              const void *residual, void *out, void *pre, int32_t *dev_status, void *stream);
+
+/* sc_linear_backward -- gradients of sc_linear.  With dz = dout act'(pre):
+ *     dx = dz w,   dw = dz^T x,   dbias_j = sum_i dz_ij
+ * (the residual's gradient is dout itself).  act'(pre) and dbias are computed in
+ * fp32; for the two products dz is rounded to type once, as the operands are
+ * (fp32 operands: split as in sc_linear).  No atomics: the same call gives the
+ * same bits.
+ *   pre        (device) z from the forward pass; ignored with SC_ACT_NONE
+ *   dx, dw, dbias (device, nullable) out, overwritten; an empty sum gives zeros
+ *   dev_status as in sc_linear
+ * Errors: SC_ERR_ARG (a workspace that is too small among them), SC_ERR_CUDA. */
+int sc_linear_backward(const sc_linear_desc *desc, const void *dout, const void *x, const void *w,
+                       const void *pre, void *dx, void *dw, void *dbias, int32_t *dev_status,
+                       void *stream);
+
+/* Workspace bytes of the two calls for this problem, or minus an SC_ERR_*
+ * status.  The operands' addresses are looked at for their alignment only: a
+ * 16-bit operand whose rows do not start on 16-byte boundaries is copied into
+ * the workspace, an fp32 operand is split there.  Host only. */
+int64_t sc_linear_workspace_bytes(const sc_linear_desc *desc, const void *x, const void *w);
+int64_t sc_linear_backward_workspace_bytes(const sc_linear_desc *desc, const void *dout,
+                                           const void *x, const void *w);
+
 #ifdef __cplusplus
 }
 #endif

@@ -22,13 +22,18 @@ SC_SCALES_ROW, SC_SCALES_BAND = 0, 1
 SC_MODE_BIPOLAR, SC_MODE_UNIPOLAR = 0, 1
 SC_ORDER_NATURAL, SC_ORDER_GRAY = 0, 1
 SC_MAX_PREC, SC_MAX_RUNGS, SC_MAX_BANDS = 8, 8, 64
+SC_F32, SC_BF16, SC_F16 = 0, 1, 2
+SC_ACT_NONE, SC_ACT_RELU, SC_ACT_GELU, SC_ACT_GELU_TANH, SC_ACT_SILU = 0, 1, 2, 3, 4
 
 # every symbol include/sc.h declares
 EXPORTS = ("sc_last_error", "sc_version", "sc_kband_tilt", "sc_build_table", "sc_table_destroy",
            "sc_build_table_variant", "sc_build_table_seq", "sc_table_info", "sc_quantize", "sc_quantize_chunked",
            "sc_assign_rows", "sc_assign_fraction", "sc_matmul", "sc_matmul_engine", "sc_matmul_workspace_bytes",
            "sc_matmul_static_ws", "sc_matmul_launches", "sc_prepare_b", "sc_prepare_b_bytes",
-           "sc_bprep_destroy", "sc_selftest_wait_limit")
+           "sc_bprep_destroy", "sc_selftest_wait_limit",
+           "sc_layer_norm", "sc_layer_norm_backward", "sc_layer_norm_workspace_bytes",
+           "sc_linear", "sc_linear_backward", "sc_linear_workspace_bytes",
+           "sc_linear_backward_workspace_bytes")
 SC_STATIC_WS_BYTES = 64 << 20
 
 
@@ -38,6 +43,24 @@ class ScMatmulDesc(ctypes.Structure):
                 ("q_dec", ctypes.c_double), ("scales", ctypes.c_int32),
                 ("mode", ctypes.c_int32), ("workspace", ctypes.c_void_p),
                 ("workspace_bytes", ctypes.c_int64), ("b_prep", ctypes.c_void_p)]
+
+
+class ScNormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("ld_x", ctypes.c_int64),
+                ("ld_y", ctypes.c_int64), ("ld_dx", ctypes.c_int64), ("ld_add", ctypes.c_int64),
+                ("eps", ctypes.c_double), ("x_type", ctypes.c_int32), ("y_type", ctypes.c_int32),
+                ("w_type", ctypes.c_int32), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_int64)]
+
+
+class ScLinearDesc(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("ld_x", ctypes.c_int64), ("ld_w", ctypes.c_int64), ("ld_out", ctypes.c_int64),
+                ("ld_res", ctypes.c_int64), ("ld_pre", ctypes.c_int64), ("ld_dx", ctypes.c_int64),
+                ("ld_dw", ctypes.c_int64), ("type", ctypes.c_int32), ("out_type", ctypes.c_int32),
+                ("bias_type", ctypes.c_int32), ("grad_type", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_int64)]
 
 
 class ScError(RuntimeError):
@@ -90,6 +113,17 @@ def load():
         lib.sc_prepare_b_bytes.restype = ctypes.c_int64
         lib.sc_bprep_destroy.argtypes = [vp]
         lib.sc_selftest_wait_limit.argtypes = [vp, i64, vp]
+        norm, lin = ctypes.POINTER(ScNormDesc), ctypes.POINTER(ScLinearDesc)
+        lib.sc_layer_norm.argtypes = [norm] + [vp] * 7
+        lib.sc_layer_norm_backward.argtypes = [norm] + [vp] * 10
+        lib.sc_layer_norm_workspace_bytes.argtypes = [norm]
+        lib.sc_layer_norm_workspace_bytes.restype = ctypes.c_int64
+        lib.sc_linear.argtypes = [lin] + [vp] * 8
+        lib.sc_linear_backward.argtypes = [lin] + [vp] * 9
+        lib.sc_linear_workspace_bytes.argtypes = [lin, vp, vp]
+        lib.sc_linear_workspace_bytes.restype = ctypes.c_int64
+        lib.sc_linear_backward_workspace_bytes.argtypes = [lin, vp, vp, vp]
+        lib.sc_linear_backward_workspace_bytes.restype = ctypes.c_int64
         for name in EXPORTS:
             getattr(lib, name).restype = getattr(lib, name).restype or ctypes.c_int
         _lib = lib
@@ -253,3 +287,45 @@ def sc_bprep_destroy(prep):
 
 def sc_selftest_wait_limit(dev_status, limit_cycles, stream=None):
     _check(load().sc_selftest_wait_limit(_ptr(dev_status), int(limit_cycles), _stream(stream)))
+
+
+def sc_layer_norm(desc: ScNormDesc, x, weight, bias, y, mean, rstd, stream=None):
+    _check(load().sc_layer_norm(ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(bias), _ptr(y),
+                                _ptr(mean), _ptr(rstd), _stream(stream)))
+
+
+def sc_layer_norm_backward(desc: ScNormDesc, dy, x, weight, mean, rstd, dx_add, dx, dweight, dbias,
+                           stream=None):
+    _check(load().sc_layer_norm_backward(ctypes.byref(desc), _ptr(dy), _ptr(x), _ptr(weight),
+                                         _ptr(mean), _ptr(rstd), _ptr(dx_add), _ptr(dx),
+                                         _ptr(dweight), _ptr(dbias), _stream(stream)))
+
+
+def sc_layer_norm_workspace_bytes(desc: ScNormDesc) -> int:
+    return _bytes(load().sc_layer_norm_workspace_bytes(ctypes.byref(desc)))
+
+
+def sc_linear(desc: ScLinearDesc, x, w, bias, residual, out, pre, dev_status, stream=None):
+    _check(load().sc_linear(ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(bias), _ptr(residual),
+                            _ptr(out), _ptr(pre), _ptr(dev_status), _stream(stream)))
+
+
+def sc_linear_backward(desc: ScLinearDesc, dout, x, w, pre, dx, dw, dbias, dev_status, stream=None):
+    _check(load().sc_linear_backward(ctypes.byref(desc), _ptr(dout), _ptr(x), _ptr(w), _ptr(pre),
+                                     _ptr(dx), _ptr(dw), _ptr(dbias), _ptr(dev_status),
+                                     _stream(stream)))
+
+
+def sc_linear_workspace_bytes(desc: ScLinearDesc, x, w) -> int:
+    return _bytes(load().sc_linear_workspace_bytes(ctypes.byref(desc), _ptr(x), _ptr(w)))
+
+
+def sc_linear_backward_workspace_bytes(desc: ScLinearDesc, dout, x, w) -> int:
+    return _bytes(load().sc_linear_backward_workspace_bytes(ctypes.byref(desc), _ptr(dout), _ptr(x),
+                                                            _ptr(w)))
+
+
+def _bytes(n: int) -> int:
+    if n < 0:
+        _check(-n)
+    return n

@@ -1,0 +1,101 @@
+// sc_layers.cuh -- element types and small device helpers shared by the
+// floating-point layers (sc_norm.cu, sc_linear.cu).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include "sc_internal.cuh"
+
+namespace scb {
+
+inline bool type_ok(int t) { return t == SC_F32 || t == SC_BF16 || t == SC_F16; }
+inline int type_size(int t) { return t == SC_F32 ? 4 : 2; }
+inline int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+inline int64_t div_up(int64_t v, int64_t by) { return (v + by - 1) / by; }
+inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
+
+// E contiguous elements to and from fp32 registers.  E * sizeof(T) is 16 or 32
+// bytes on a 16-byte boundary, 8 bytes on an 8-byte boundary, or one element.
+template <typename T, int E>
+__device__ __forceinline__ void load_vec(const T *p, float (&v)[E]) {
+    constexpr int B = E * (int)sizeof(T);
+    if constexpr (E == 1) {
+        v[0] = to_f(*p);
+    } else {
+        static_assert(B == 8 || B % 16 == 0, "vector width");
+        constexpr int W = B == 8 ? 2 : 4;  // 32-bit words per load
+        uint32_t raw[B / 4];
+#pragma unroll
+        for (int i = 0; i < B / 4 / W; ++i) {
+            if constexpr (W == 4)
+                reinterpret_cast<uint4 *>(raw)[i] = reinterpret_cast<const uint4 *>(p)[i];
+            else
+                reinterpret_cast<uint2 *>(raw)[i] = reinterpret_cast<const uint2 *>(p)[i];
+        }
+        const T *e = reinterpret_cast<const T *>(raw);
+#pragma unroll
+        for (int i = 0; i < E; ++i) v[i] = to_f(e[i]);
+    }
+}
+
+template <typename T, int E>
+__device__ __forceinline__ void store_vec(T *p, const float (&v)[E]) {
+    constexpr int B = E * (int)sizeof(T);
+    if constexpr (E == 1) {
+        *p = from_f<T>(v[0]);
+    } else {
+        static_assert(B == 8 || B % 16 == 0, "vector width");
+        constexpr int W = B == 8 ? 2 : 4;
+        alignas(16) T e[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) e[i] = from_f<T>(v[i]);
+#pragma unroll
+        for (int i = 0; i < B / 4 / W; ++i) {
+            if constexpr (W == 4)
+                reinterpret_cast<uint4 *>(p)[i] = reinterpret_cast<const uint4 *>(e)[i];
+            else
+                reinterpret_cast<uint2 *>(p)[i] = reinterpret_cast<const uint2 *>(e)[i];
+        }
+    }
+}
+
+// The same with the element type known at run time (uniform over the block):
+// parameters, which are read far less often than activations.
+template <int E>
+__device__ __forceinline__ void load_any(const void *p, int type, int64_t i, float (&v)[E]) {
+    if (type == SC_F32) load_vec<float, E>(static_cast<const float *>(p) + i, v);
+    else if (type == SC_BF16) load_vec<__nv_bfloat16, E>(static_cast<const __nv_bfloat16 *>(p) + i, v);
+    else load_vec<__half, E>(static_cast<const __half *>(p) + i, v);
+}
+__device__ __forceinline__ void store_any(void *p, int type, int64_t i, float v) {
+    if (type == SC_F32) static_cast<float *>(p)[i] = v;
+    else if (type == SC_BF16) static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
+    else static_cast<__half *>(p)[i] = __float2half_rn(v);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Column sums from per-block partial sums (sc_norm.cu): out_k[c] = sum_p
+// part[p][k][c], k < n_out, c < cols, in ascending p.  A null out_k is skipped.
+int launch_finish_columns(const float *part, int n_part, int n_out, int64_t cols, void *out0,
+                          void *out1, int out_type, cudaStream_t stream);
+
+}  // namespace scb

@@ -182,6 +182,252 @@ def matmul(a_lv, a_s, b_lv, b_s, rung, perm, offs, table: ScTable, *, op=L.SC_OP
     return out, counts
 
 
+# ---- floating-point layers of a transformer block ---------------------------------
+# Matrices are given as [..., columns] tensors whose rows lie one fixed stride apart
+# (contiguous, or a view such as x[:, 0] or x[:, :n]); anything else is refused rather
+# than copied.  Work goes to `stream`, or to torch's current stream of the tensors' device.
+
+_TYPES = {torch.float32: L.SC_F32, torch.bfloat16: L.SC_BF16, torch.float16: L.SC_F16}
+ACTIVATIONS = {"none": L.SC_ACT_NONE, "relu": L.SC_ACT_RELU, "gelu": L.SC_ACT_GELU,
+               "gelu_tanh": L.SC_ACT_GELU_TANH, "silu": L.SC_ACT_SILU}
+
+
+def _type(dtype, what: str) -> int:
+    try:
+        return _TYPES[dtype]
+    except KeyError:
+        raise ValueError(f"{what} must be float32, bfloat16 or float16, not {dtype}") from None
+
+
+def _matrix(t: torch.Tensor, what: str, like: torch.Tensor = None, shape=None, dtype=None):
+    """(rows, columns, row stride) of a [..., columns] CUDA tensor."""
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if like is not None and t.device != like.device:
+        raise ValueError(f"{what} is on {t.device}, not on {like.device}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}, not {t.dtype}")
+    if t.dim() == 0:
+        raise ValueError(f"{what} must have at least one dimension")
+    cols = t.shape[-1]
+    if t.is_contiguous():
+        return (t.numel() // cols if cols else 0), cols, cols
+    if cols > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{what}: elements of a row must be contiguous")
+    rows, ld = 1, None
+    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
+            continue
+        if ld is None:
+            ld = st
+        elif st != rows * ld:
+            raise ValueError(f"{what}: rows must lie one fixed stride apart")
+        rows *= n
+    ld = cols if ld is None else ld
+    if ld < cols:
+        raise ValueError(f"{what}: rows overlap (stride {ld} for {cols} columns)")
+    return rows, cols, ld
+
+
+def _vector(t, n: int, what: str, like: torch.Tensor, dtype=None):
+    if t is None:
+        return
+    if t.device != like.device or not t.is_contiguous() or t.shape != (n,):
+        raise ValueError(f"{what} must be a contiguous [{n}] tensor on {like.device}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}, not {t.dtype}")
+
+
+def _elsewhere(t: torch.Tensor, stream) -> bool:
+    return stream is not None or t.device.index != torch.cuda.current_device()
+
+
+class _On:
+    """Makes a device, and a stream if one is given, current."""
+
+    def __init__(self, device, stream):
+        self.dev = torch.cuda.device(device)
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=device)
+        self.st = torch.cuda.stream(stream) if stream is not None else None
+
+    def __enter__(self):
+        self.dev.__enter__()
+        if self.st is not None:
+            self.st.__enter__()
+
+    def __exit__(self, *exc):
+        if self.st is not None:
+            self.st.__exit__(*exc)
+        self.dev.__exit__(*exc)
+
+
+def _scratch(desc, need: int, workspace, like: torch.Tensor):
+    """Puts a workspace of `need` bytes into the descriptor; the caller keeps the
+    returned tensor until the call is enqueued."""
+    if need <= 0:
+        return None
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+    elif workspace.device != like.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
+    desc.workspace = workspace.data_ptr()
+    desc.workspace_bytes = workspace.numel() * workspace.element_size()
+    return workspace
+
+
+def _act_code(act) -> int:
+    if isinstance(act, str):
+        if act not in ACTIVATIONS:
+            raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, not {act!r}")
+        return ACTIVATIONS[act]
+    return int(act)
+
+
+def layer_norm(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-6, *, out_dtype=None,
+               want_stats: bool = False, out=None, stream=None):
+    """Layer norm over the last axis: x [..., D] -> (y, mean, rstd).
+
+    weight, bias: [D] of one type, or None.  y has out_dtype (x's by default; fp32 may
+    become 16 bits and back, e.g. fp32 for quantize() after a bf16 block).  mean and rstd
+    (fp32, x.shape[:-1]) are returned with want_stats, for layer_norm_backward, and are
+    None otherwise.  out: the tensor to write, which may be x itself (same type)."""
+    rows, D, ld = _matrix(x, "x")
+    if _elsewhere(x, stream):
+        with _On(x.device, stream):
+            return layer_norm(x, weight, bias, eps, out_dtype=out_dtype, want_stats=want_stats, out=out)
+    _vector(weight, D, "weight", x)
+    _vector(bias, D, "bias", x, None if weight is None else weight.dtype)
+    if out is None:
+        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+    _, _, ld_y = _matrix(out, "out", x, x.shape, out_dtype)
+    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if want_stats else None
+    rstd = torch.empty_like(mean) if want_stats else None
+    p = weight if weight is not None else bias
+    d = L.ScNormDesc(rows, D, ld, ld_y, 0, 0, eps, _type(x.dtype, "x"), _type(out.dtype, "out"),
+                     L.SC_F32 if p is None else _type(p.dtype, "weight and bias"))
+    L.sc_layer_norm(d, x, weight, bias, out, mean, rstd, torch.cuda.current_stream())
+    return out, mean, rstd
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                        weight=None, *, dx_add=None, want_dx: bool = True, want_params=None,
+                        param_dtype=None, workspace=None, stream=None):
+    """Gradients of layer_norm: (dx, dweight, dbias).
+
+    mean, rstd: from layer_norm.  dx_add (x's type and shape): a gradient added to dx
+    before its one rounding, the one that reaches x on the residual path.  dweight and
+    dbias ([D], the weight's type or param_dtype) are computed when want_params, by
+    default when there is a weight, and are None otherwise.  workspace: device scratch
+    of sc_layer_norm_workspace_bytes, allocated when None."""
+    rows, D, ld = _matrix(x, "x")
+    if _elsewhere(x, stream):
+        with _On(x.device, stream):
+            return layer_norm_backward(dy, x, mean, rstd, weight, dx_add=dx_add, want_dx=want_dx,
+                                       want_params=want_params, param_dtype=param_dtype,
+                                       workspace=workspace)
+    _, _, ld_y = _matrix(dy, "dy", x, x.shape)
+    for t, what in ((mean, "mean"), (rstd, "rstd")):
+        if t.dtype != torch.float32 or t.device != x.device or t.numel() != rows or not t.is_contiguous():
+            raise ValueError(f"{what} must be a contiguous float32 tensor of {rows} values on {x.device}")
+    _vector(weight, D, "weight", x)
+    if want_params is None:
+        want_params = weight is not None
+    if weight is not None and param_dtype is not None and param_dtype != weight.dtype:
+        raise ValueError("dweight and dbias have the weight's type")
+    pt = weight.dtype if weight is not None else (param_dtype or torch.float32)
+    ld_add = 0
+    if dx_add is not None:
+        _, _, ld_add = _matrix(dx_add, "dx_add", x, x.shape, x.dtype)
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if want_dx else None
+    dw = torch.empty(D, dtype=pt, device=x.device) if want_params else None
+    db = torch.empty_like(dw) if want_params else None
+    d = L.ScNormDesc(rows, D, ld, ld_y, D, ld_add, 0.0, _type(x.dtype, "x"), _type(dy.dtype, "dy"),
+                     _type(pt, "weight"))
+    ws = _scratch(d, L.sc_layer_norm_workspace_bytes(d) if want_params else 0, workspace, x)
+    L.sc_layer_norm_backward(d, dy, x, weight, mean, rstd, dx_add, dx, dw, db,
+                             torch.cuda.current_stream())
+    del ws
+    return dx, dw, db
+
+
+def linear(x: torch.Tensor, w: torch.Tensor, bias=None, residual=None, act="none", *, out_dtype=None,
+           want_pre: bool = False, out=None, workspace=None, dev_status=None, stream=None):
+    """act(x w^T + bias) + residual in one matrix product: (out, pre).
+
+    x [..., K] and w [N, K] of one type (bf16 and fp16 run on the tensor cores as they
+    are, fp32 as three bf16 parts); bias [N] of any type; residual and out [..., N] of
+    out_dtype, which is x's type (default) or float32.  act: a key of ACTIVATIONS.  pre
+    is x w^T + bias in x's type with want_pre (what linear_backward needs for an
+    activation), else None.  out: the tensor to write, which may be the residual."""
+    M, K, ld_x = _matrix(x, "x")
+    if _elsewhere(x, stream):
+        with _On(x.device, stream):
+            return linear(x, w, bias, residual, act, out_dtype=out_dtype, want_pre=want_pre, out=out,
+                          workspace=workspace, dev_status=dev_status)
+    if w.dim() != 2:
+        raise ValueError(f"w has shape {tuple(w.shape)}, not [N, {K}]")
+    N = w.shape[0]
+    _, _, ld_w = _matrix(w, "w", x, (N, K), x.dtype)
+    _vector(bias, N, "bias", x)
+    shape = x.shape[:-1] + (N,)
+    ld_res = 0
+    if residual is not None:
+        _, _, ld_res = _matrix(residual, "residual", x, shape, out_dtype or x.dtype)
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype or x.dtype, device=x.device)
+    _, _, ld_out = _matrix(out, "out", x, shape, out_dtype or x.dtype)
+    pre = torch.empty(shape, dtype=x.dtype, device=x.device) if want_pre else None
+    d = L.ScLinearDesc(M, N, K, ld_x, ld_w, ld_out, ld_res, N, 0, 0, _type(x.dtype, "x"),
+                       _type(out.dtype, "out"),
+                       L.SC_F32 if bias is None else _type(bias.dtype, "bias"), 0, _act_code(act))
+    ws = _scratch(d, L.sc_linear_workspace_bytes(d, x, w), workspace, x)
+    L.sc_linear(d, x, w, bias, residual, out, pre, dev_status, torch.cuda.current_stream())
+    del ws
+    return out, pre
+
+
+def linear_backward(dout: torch.Tensor, x: torch.Tensor, w: torch.Tensor, pre=None, act="none", *,
+                    want_dx: bool = True, want_dw: bool = True, want_db: bool = True,
+                    grad_dtype=None, workspace=None, dev_status=None, stream=None):
+    """Gradients of linear: (dx, dw, db), each None where it is not wanted.
+
+    dout [..., N] of x's type or float32; pre as linear returned it (needed with an
+    activation).  dx has x's type, dw and db grad_dtype (w's type by default).  The
+    residual's gradient is dout itself."""
+    M, K, ld_x = _matrix(x, "x")
+    if _elsewhere(x, stream):
+        with _On(x.device, stream):
+            return linear_backward(dout, x, w, pre, act, want_dx=want_dx, want_dw=want_dw,
+                                   want_db=want_db, grad_dtype=grad_dtype, workspace=workspace,
+                                   dev_status=dev_status)
+    if w.dim() != 2:
+        raise ValueError(f"w has shape {tuple(w.shape)}, not [N, {K}]")
+    N = w.shape[0]
+    _, _, ld_w = _matrix(w, "w", x, (N, K), x.dtype)
+    shape = x.shape[:-1] + (N,)
+    _, _, ld_out = _matrix(dout, "dout", x, shape)
+    code = _act_code(act)
+    ld_pre = 0
+    if code != L.SC_ACT_NONE:
+        if pre is None:
+            raise ValueError("an activation's gradient needs pre")
+        _, _, ld_pre = _matrix(pre, "pre", x, shape, x.dtype)
+    gt = grad_dtype or w.dtype
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if want_dx else None
+    dw = torch.empty(N, K, dtype=gt, device=x.device) if want_dw else None
+    db = torch.empty(N, dtype=gt, device=x.device) if want_db else None
+    d = L.ScLinearDesc(M, N, K, ld_x, ld_w, ld_out, 0, ld_pre, K, K, _type(x.dtype, "x"),
+                       _type(dout.dtype, "dout"), 0, _type(gt, "grad_dtype"), code)
+    ws = _scratch(d, L.sc_linear_backward_workspace_bytes(d, dout, x, w), workspace, x)
+    L.sc_linear_backward(d, dout, x, w, pre if code else None, dx, dw, db, dev_status,
+                         torch.cuda.current_stream())
+    del ws
+    return dx, dw, db
+
+
 class ScStep:
     """All device buffers of one workload, and the full hot-path step:
     quantise A (+ row statistic), quantise B, assign rows (rung-sorted order),
