@@ -319,7 +319,8 @@ def test_linear(M, N, K, t, ot):
 
 
 @pytest.mark.parametrize("t,ot", LIN_TYPES)
-@pytest.mark.parametrize("M,N,K", [(700, 1536, 512), (2100, 768, 256), (4112, 512, 264)])
+@pytest.mark.parametrize("M,N,K", [(700, 1536, 512), (2100, 768, 256), (4112, 512, 264), (4112, 1600, 136),
+                                   (2600, 2051, 1250)])
 def test_linear_many_tiles(M, N, K, t, ot):
     g = gen(M + N + K)
     x, w = rnd(g, M, K, dtype=t), rnd(g, N, K, dtype=t, scale=K ** -0.5)
@@ -438,10 +439,11 @@ def test_linear_backward_activations(act, t):
 
 
 @pytest.mark.parametrize("t,ot", LIN_TYPES)
-def test_linear_backward_many_tiles(t, ot):
+@pytest.mark.parametrize("M,N,K", [(2056, 1536, 768), (2313, 2304, 2050)])
+def test_linear_backward_many_tiles(M, N, K, t, ot):
     g = gen(22)
-    x, w = rnd(g, 2056, 768, dtype=t), rnd(g, 1536, 768, dtype=t, scale=0.05)
-    check_linear_backward(rnd(g, 2056, 1536, dtype=ot), x, w, rnd(g, 2056, 1536, dtype=t), "gelu_tanh")
+    x, w = rnd(g, M, K, dtype=t), rnd(g, N, K, dtype=t, scale=0.05)
+    check_linear_backward(rnd(g, M, N, dtype=ot), x, w, rnd(g, M, N, dtype=t), "gelu_tanh")
 
 
 def test_linear_backward_options():
