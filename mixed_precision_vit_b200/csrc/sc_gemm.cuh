@@ -31,31 +31,36 @@ int launch_gemm(int64_t M, int64_t N, int64_t K, int type16, const GemmOperand &
                 cudaStream_t stream);
 
 // ---- activations ------------------------------------------------------------
-__device__ __forceinline__ float act_fn(float z, int act) {
-    switch (act) {
-        case SC_ACT_RELU: return z > 0.f ? z : (z == z ? 0.f : z);
-        case SC_ACT_GELU: return 0.5f * z * (1.f + erff(z * 0.70710678f));
-        case SC_ACT_GELU_TANH: return 0.5f * z * (1.f + tanhf(0.79788456f * (z + 0.044715f * z * z * z)));
-        case SC_ACT_SILU: return z / (1.f + expf(-z));
-        default: return z;
-    }
+// 1 / (1 + exp(-x)) times n.  The intrinsics' errors (2 ulp of the quotient, a
+// few of exp where the result is far below |n|) stay under 2^-21 |n|.
+__device__ __forceinline__ float times_sigmoid(float n, float x) { return __fdividef(n, 1.f + __expf(-x)); }
+
+// sqrt(8 / pi) (z + 0.044715 z^3): gelu_tanh is z sigmoid of it
+__device__ __forceinline__ float gelu_tanh_arg(float z) { return 1.59576912f * z * (1.f + 0.044715f * z * z); }
+
+template <int ACT>
+__device__ __forceinline__ float act_fn(float z) {
+    if constexpr (ACT == SC_ACT_RELU) return z < 0.f ? 0.f : z;  // keeps a NaN
+    if constexpr (ACT == SC_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678f));
+    if constexpr (ACT == SC_ACT_GELU_TANH) return times_sigmoid(z, gelu_tanh_arg(z));
+    if constexpr (ACT == SC_ACT_SILU) return times_sigmoid(z, z);
+    return z;
 }
 
-__device__ __forceinline__ float act_grad(float z, int act) {
-    switch (act) {
-        case SC_ACT_RELU: return z > 0.f ? 1.f : (z == z ? 0.f : z);
-        case SC_ACT_GELU:
-            return 0.5f * (1.f + erff(z * 0.70710678f)) + z * 0.39894228f * expf(-0.5f * z * z);
-        case SC_ACT_GELU_TANH: {
-            const float t = tanhf(0.79788456f * (z + 0.044715f * z * z * z));
-            return 0.5f * (1.f + t) + 0.5f * z * (1.f - t * t) * 0.79788456f * (1.f + 0.134145f * z * z);
-        }
-        case SC_ACT_SILU: {
-            const float q = 1.f / (1.f + expf(-z));
-            return q * (1.f + z * (1.f - q));
-        }
-        default: return 1.f;
+template <int ACT>
+__device__ __forceinline__ float act_grad(float z) {
+    if constexpr (ACT == SC_ACT_RELU) return z > 0.f ? 1.f : (z == z ? 0.f : z);
+    if constexpr (ACT == SC_ACT_GELU)
+        return 0.5f * (1.f + erff(z * 0.70710678f)) + z * 0.39894228f * __expf(-0.5f * z * z);
+    if constexpr (ACT == SC_ACT_GELU_TANH) {
+        const float q = times_sigmoid(1.f, gelu_tanh_arg(z));
+        return q + z * q * (1.f - q) * 1.59576912f * (1.f + 0.134145f * z * z);
     }
+    if constexpr (ACT == SC_ACT_SILU) {
+        const float q = times_sigmoid(1.f, z);
+        return q * (1.f + z * (1.f - q));
+    }
+    return 1.f;
 }
 
 }  // namespace scb

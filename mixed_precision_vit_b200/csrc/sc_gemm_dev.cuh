@@ -1,0 +1,644 @@
+// sc_gemm_dev.cuh -- the kernels of sc_gemm.cu: D(m, n) = sum_k A(m, k) B(n, k) on the 5th-generation tensor
+// cores (tcgen05.mma.kind::f16, fp32 accumulators in tensor memory), with the
+// linear layer's epilogue.
+//
+// Operand tiles of 64 contraction indexes (128 bytes, 128-byte swizzle) come
+// by TMA into a ring of shared-memory stages; rows and columns past the
+// matrices' ends read as zeros.  Either operand may have k or its own index
+// contiguous (the shared-memory descriptor covers both), so the forward pass
+// (x w^T), dz w and dz^T x run the same kernel without transposing anything.
+//
+// fp32 operands: x = x1 + x2 + x3 exactly, bf16 parts of 8 bits of
+// significand, |x2| <= 2^-8 |x|, |x3| <= 2^-16 |x|.  Of the nine products the
+// three below 2^-24 |x w| are left out; the others run as six products over
+// the planes, the small ones first.
+//
+// The tensor cores cut an fp32 sum where fp32 arithmetic rounds, so a long sum
+// drifts towards zero by about 2^-25 of itself per 16 indexes.  Where the
+// result keeps fp32, an accumulator therefore takes CHUNK stages at most, and
+// the epilogue warps add the chunks in registers.
+//
+// Kernels:
+//   gemm_kernel<2>  clusters of two CTAs on two SMs, one cta_group::2 MMA of
+//                   256 rows x bn columns; persistent over the tiles, two
+//                   accumulators, so a tile's epilogue runs under the next
+//                   tile's products
+//   gemm_kernel<1>  the same with one CTA and 128 rows
+//   gemm_split_kernel  few tiles: a cluster of CTAs shares one tile's
+//                   contraction and adds the parts over distributed shared
+//                   memory, in rank order
+// All waits are bounded, as in the count engine: on expiry the kernel records
+// SC_DEV_WAIT_LIMIT, waits for its own copies and products, frees tensor
+// memory and returns.
+#pragma once
+#include <cuda.h>
+
+#include "sc_gemm.cuh"
+#include "sc_tc_dev.cuh"
+
+namespace scb {
+namespace gemm {
+
+using namespace tcd;
+
+constexpr int GK = 64;                  // contraction indexes per stage
+constexpr int GM = 128;                 // rows per CTA
+constexpr int A_STAGE = GM * GK * 2;    // 16 KB
+constexpr int EPI_WARPS = 8;            // two per quadrant of tensor-memory lanes
+constexpr int EPI_WARP0 = 4;
+constexpr int GEMM_THREADS = (EPI_WARP0 + EPI_WARPS) * 32;
+constexpr int RING_BYTES = 160 * 1024;  // 5 stages of 32 KB
+constexpr int MAX_RING = 8;
+constexpr int CHUNK = 16;               // stages (1024 indexes) per accumulation of an fp32 result
+// Epilogue staging, per warp: 32 rows x 64 columns of fp32, 16-byte quads
+// permuted so that both a lane's row (written) and 8 lanes' row (read) touch
+// every bank once.
+constexpr int STG_COLS = 64;
+constexpr int STG_BYTES = 32 * STG_COLS * 4;
+constexpr int ACC_COLS = 256;           // tensor-memory columns per accumulator buffer
+constexpr int GN_MAX = 256;            // columns per tile
+constexpr int SPLIT_N = 128;            // columns of a tile whose contraction is shared
+constexpr int SPLIT_LD = SPLIT_N + 4;
+static_assert(GM * SPLIT_LD * 4 <= RING_BYTES, "parts of a shared tile fit the ring");
+
+struct GemmArgs {
+    CUtensorMap ma, mb;
+    int64_t ld_out, ld_res, ld_pre;
+    const void *bias, *res;
+    void *out, *pre;
+    int32_t *dev_status;
+    int M, N;
+    int n_k;            // stages of one product
+    int n_prod;         // 1, or 6 for fp32 operands
+    int chunk;          // stages per accumulation
+    int a_mn, b_mn;     // operand has its own index contiguous
+    int bn;             // columns per tile
+    int n_tiles_n, n_tiles;
+    int stages, b_stage, b_box_rows;
+    uint32_t idesc;
+    int bias_type, out_type, pre_type;
+    int vec;            // 8 columns per access everywhere
+};
+
+struct GemmSync {
+    uint64_t full[MAX_RING], empty[MAX_RING];
+    uint64_t acc_full[2], acc_empty[2];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+constexpr int GEMM_SMEM = RING_BYTES + EPI_WARPS * STG_BYTES + 1024 + 512;
+static_assert(sizeof(GemmSync) <= 512, "barriers");
+static_assert(GEMM_SMEM <= 227 * 1024, "shared memory");
+
+// The parts of fp32 operands that product `i` multiplies, small ones first.
+__device__ __forceinline__ int plane_a(int i, int n) { return n == 1 ? 0 : (0x001102 >> (4 * i)) & 15; }
+__device__ __forceinline__ int plane_b(int i, int n) { return n == 1 ? 0 : (0x010120 >> (4 * i)) & 15; }
+
+// A slot of the ring of stages and the parity of its current use.
+struct Ring {
+    int slot;
+    uint32_t phase;
+    __device__ __forceinline__ void next(int stages) {
+        if (++slot == stages) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+    __device__ __forceinline__ void back(int n, int stages) {  // n <= stages
+        slot -= n;
+        if (slot < 0) {
+            slot += stages;
+            phase ^= 1;
+        }
+    }
+};
+
+// 128-byte swizzled operand: 8-row groups (k_major: of rows, else of k) 1024
+// bytes apart; 64-column blocks of the operand's own index 8192 bytes apart.
+__device__ __forceinline__ uint64_t swizzled_desc(uint32_t saddr, bool mn) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(mn ? 8192 >> 4 : 1) << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+template <int CG>
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc, uint32_t acc) {
+    if constexpr (CG == 2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(da), "l"(db), "r"(idesc), "r"(acc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(da), "l"(db), "r"(idesc), "r"(acc)
+            : "memory");
+}
+
+// One box into this CTA's shared memory; CG = 2: its bytes count on the
+// barrier of the cluster's first CTA (`bar` is a cluster address).  No
+// multicast.
+template <int CG>
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2) {
+    if constexpr (CG == 2)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+            "l"(map), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+            "l"(map), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+            : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+    return r;
+}
+
+// The operand tile of `rows` rows (a multiple of 64 when the operand's own
+// index is contiguous) at row r0, contraction index k0.
+template <int CG>
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap *map, uint32_t bar, bool mn, int rows,
+                                          int r0, int k0, int plane) {
+    if (!mn) {
+        tma_load<CG>(dst, map, bar, k0, r0, plane);
+    } else {
+        for (int i = 0; i < rows; i += 64) tma_load<CG>(dst + i * 128, map, bar, r0 + i, k0, plane);
+    }
+}
+
+// Products of one stage: 4 MMAs of 16 contraction indexes.
+template <int CG>
+__device__ __forceinline__ void stage_mmas(const GemmArgs &p, uint32_t d, uint32_t sa, bool first) {
+    const uint32_t sb = sa + A_STAGE;
+    const uint32_t ka = p.a_mn ? 2048u : 32u, kb = p.b_mn ? 2048u : 32u;
+#pragma unroll
+    for (int k = 0; k < GK / 16; ++k)
+        mma_f16_ss<CG>(d, swizzled_desc(sa + k * ka, p.a_mn), swizzled_desc(sb + k * kb, p.b_mn), p.idesc,
+                       !(first && k == 0));
+}
+
+// Epilogue of one element.
+template <int ACT>
+__device__ __forceinline__ void epilogue1(const GemmArgs &p, float z, float bias, int64_t row, int col) {
+    float v[1] = {z + bias};
+    if (p.pre) store_any(p.pre, p.pre_type, row * p.ld_pre + col, v[0]);
+    v[0] = act_fn<ACT>(v[0]);
+    if (p.res) {
+        float r[1];
+        load_any<1>(p.res, p.out_type, row * p.ld_res + col, r);
+        v[0] += r[0];
+    }
+    store_any(p.out, p.out_type, row * p.ld_out + col, v[0]);
+}
+
+template <typename T, int R>
+__device__ __forceinline__ void load_rows(const T *p, int64_t step, const bool (&in)[R], float (&v)[R][8]) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        if (in[r]) load_vec<T, 8>(p + r * step, v[r]);
+}
+template <typename T, int R>
+__device__ __forceinline__ void store_rows(T *p, int64_t step, const bool (&in)[R], const float (&v)[R][8]) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        if (in[r]) store_vec<T, 8>(p + r * step, v[r]);
+}
+template <int R>
+__device__ __forceinline__ void store_rows_any(void *p, int type, int64_t at, int64_t step, const bool (&in)[R],
+                                               const float (&v)[R][8]) {
+    if (type == SC_F32) store_rows<float, R>(static_cast<float *>(p) + at, step, in, v);
+    else if (type == SC_BF16) store_rows<__nv_bfloat16, R>(static_cast<__nv_bfloat16 *>(p) + at, step, in, v);
+    else store_rows<__half, R>(static_cast<__half *>(p) + at, step, in, v);
+}
+
+// Epilogue of columns col .. col + 7 (their bias: b) of R rows, row + i step.
+// Every step runs over all of them before the next one begins: the few warps
+// of an epilogue hide latency by independent work, not by each other.
+template <int ACT, int R>
+__device__ __forceinline__ void epilogue_rows(const GemmArgs &p, float (&v)[R][8], const float (&b)[8], int64_t row,
+                                              int step, int col) {
+    bool in[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) in[r] = row + r * step < p.M;
+    float a[R][8];
+    if (p.res) {
+        const int64_t at = row * p.ld_res + col, st = step * p.ld_res;
+        if (p.out_type == SC_F32) load_rows<float, R>(static_cast<const float *>(p.res) + at, st, in, a);
+        else if (p.out_type == SC_BF16) load_rows<__nv_bfloat16, R>(static_cast<const __nv_bfloat16 *>(p.res) + at, st, in, a);
+        else load_rows<__half, R>(static_cast<const __half *>(p.res) + at, st, in, a);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[r][i] += b[i];
+    if (p.pre) store_rows_any<R>(p.pre, p.pre_type, row * p.ld_pre + col, step * p.ld_pre, in, v);
+    if constexpr (ACT != SC_ACT_NONE) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[r][i] = act_fn<ACT>(v[r][i]);
+    }
+    if (p.res) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[r][i] += a[r][i];
+    }
+    store_rows_any<R>(p.out, p.out_type, row * p.ld_out + col, step * p.ld_out, in, v);
+}
+
+// tcgen05.ld without its wait; the registers are valid after tmem_wait_ld.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+          "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]),
+          "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]),
+          "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[i]));  // no use before the wait
+}
+
+template <int CG>
+__device__ __forceinline__ void tmem_alloc(uint32_t *where) {
+    if constexpr (CG == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(where)),
+                     "r"(TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(where)),
+                     "r"(TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+}
+template <int CG>
+__device__ __forceinline__ void tmem_free(uint32_t base) {
+    if constexpr (CG == 2)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(TMEM_COLS) : "memory");
+    else
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(TMEM_COLS) : "memory");
+}
+
+// CG CTAs per tile of CG * 128 rows.  SPLIT (CG = 1): the CTAs of a cluster
+// each take a share of one tile's contraction.  KEEP: accumulations of p.chunk stages added in registers.
+template <int CG, bool SPLIT, bool KEEP, int ACT>
+__global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_constant__ GemmArgs p) {
+    static_assert(CG == 1 || !SPLIT, "a shared contraction has one CTA per part");
+    static_assert(KEEP || !SPLIT, "parts are added in fp32");
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    uint8_t *ring = smem_raw + (base - smem_addr(smem_raw));
+    GemmSync &sy = *reinterpret_cast<GemmSync *>(ring + RING_BYTES + EPI_WARPS * STG_BYTES);
+    volatile int *abort_flag = &sy.abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = CG == 2 || SPLIT ? (int)cluster_rank() : 0;
+    const int first_tile = CG == 2 || SPLIT ? (int)cluster_id() : (int)blockIdx.x;
+    const int tile_step = SPLIT ? p.n_tiles : CG == 2 ? (int)cluster_count() : (int)gridDim.x;
+    // this CTA's share of the stages of a tile
+    const int n_it = p.n_k * p.n_prod;
+    int it0 = 0, it1 = n_it;
+    if constexpr (SPLIT) {
+        const int parts = (int)gridDim.x / p.n_tiles;
+        it0 = (int)((int64_t)n_it * rank / parts);
+        it1 = (int)((int64_t)n_it * (rank + 1) / parts);
+    }
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < MAX_RING; ++s) {
+            mbar_init(&sy.full[s], 1);
+            mbar_init(&sy.empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&sy.acc_full[b], 1);
+            mbar_init(&sy.acc_empty[b], CG * EPI_WARPS);
+        }
+        mbar_init(&sy.drain, 1);
+        sy.abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 2) tmem_alloc<CG>(&sy.tmem_base);
+    tc_fence_before();
+    __syncthreads();
+    if (CG == 2) cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = sy.tmem_base;
+    const int stage_bytes = A_STAGE + p.b_stage;
+    auto epilogue = [&]() {
+        // ================= epilogue =================
+        // Warps e and e + 4 share a quadrant of tensor-memory lanes (32 rows)
+        // and take half of the columns each.
+        const int e = warp - EPI_WARP0, quad = warp & 3;
+        const int half = p.bn / 2, c_lo = (e >> 2) * half;
+        float *stg = reinterpret_cast<float *>(ring + RING_BYTES + e * STG_BYTES);
+        const int lc = lane & 7, lr = lane >> 3;
+        // 64 columns of the warp's rows: through shared memory, so that 8 lanes
+        // access one row's 64 columns together
+        auto stage_quad = [&](int j, float a, float b, float c, float d) {
+            const int at = ((j & 1) * 8 + (j >> 1)) ^ (lane & 7);
+            *reinterpret_cast<float4 *>(stg + lane * STG_COLS + at * 4) = make_float4(a, b, c, d);
+        };
+        auto store_staged = [&](int64_t row0, int col0) {
+            __syncwarp();
+            if (p.vec) {
+                const int col = col0 + lc * 8;
+                if (col < p.N) {
+                    float b[8] = {};
+                    if (p.bias) load_any<8>(p.bias, p.bias_type, col, b);
+                    constexpr int R = 4;
+#pragma unroll 1
+                    for (int r = lr; r < 32; r += 4 * R) {
+                        float o[R][8];
+#pragma unroll
+                        for (int k = 0; k < R; ++k) {
+                            const int rr = r + 4 * k;
+                            const float *q = stg + rr * STG_COLS;
+                            const float4 x = *reinterpret_cast<const float4 *>(q + (lc ^ (rr & 7)) * 4);
+                            const float4 y = *reinterpret_cast<const float4 *>(q + (8 + (lc ^ (rr & 7))) * 4);
+                            o[k][0] = x.x; o[k][1] = x.y; o[k][2] = x.z; o[k][3] = x.w;
+                            o[k][4] = y.x; o[k][5] = y.y; o[k][6] = y.z; o[k][7] = y.w;
+                        }
+                        epilogue_rows<ACT, R>(p, o, b, row0 + r, 4, col);
+                    }
+                }
+            } else {
+                // rows on no 16-byte boundary: one column per lane
+                for (int h = 0; h < STG_COLS; h += 32) {
+                    const int c = h + lane, j = c >> 2, col = col0 + c;
+                    if (col >= p.N) break;
+                    float b[1] = {0.f};
+                    if (p.bias) load_any<1>(p.bias, p.bias_type, col, b);
+                    const int at = (j & 1) * 8 + (j >> 1);
+                    const int rows = (int)min((int64_t)32, p.M - row0);
+#pragma unroll 4
+                    for (int r = 0; r < rows; ++r)
+                        epilogue1<ACT>(p, stg[r * STG_COLS + (at ^ (r & 7)) * 4 + (c & 3)], b[0], row0 + r, col);
+                }
+            }
+            __syncwarp();
+        };
+        auto release = [&](int buf) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (CG == 2) mbar_arrive_cluster(&sy.acc_empty[buf], 0);
+                else mbar_arrive(&sy.acc_empty[buf]);
+            }
+        };
+        uint32_t n = 0;
+        for (int t = first_tile; t < p.n_tiles; t += tile_step) {
+            const int64_t row0 = (int64_t)(t / p.n_tiles_n) * (CG * GM) + (CG == 2 ? rank * GM : 0) + quad * 32;
+            const int n0 = (t % p.n_tiles_n) * p.bn + c_lo;
+            const uint32_t lane_acc = tmem + c_lo + ((uint32_t)(quad * 32) << 16);
+            if constexpr (KEEP) {
+                // add up the chunks: this lane's row, columns c_lo .. c_lo + half
+                constexpr int COLS = SPLIT ? SPLIT_N / 2 : GN_MAX / 2;
+                float v[COLS] = {};
+                for (int i = it0; i < it1; i += p.chunk, ++n) {
+                    const int buf = n & 1;
+                    if (!wait_warp(&sy.acc_full[buf], (n >> 1) & 1, abort_flag)) return;
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < COLS; c += 32) {
+                        if (c < half) {
+                            uint32_t r[32];
+                            tmem_ld32(lane_acc + buf * ACC_COLS + c, r);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[c + j] += __uint_as_float(r[j]);
+                        }
+                    }
+                    release(buf);
+                }
+                if constexpr (SPLIT) {
+                    float *part = reinterpret_cast<float *>(ring) + (quad * 32 + lane) * SPLIT_LD + c_lo;
+#pragma unroll
+                    for (int c = 0; c < COLS; c += 4)
+                        if (c < half)
+                            *reinterpret_cast<float4 *>(part + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < COLS; c += STG_COLS) {
+                        if (c >= half) break;
+#pragma unroll
+                        for (int j = 0; j < STG_COLS / 4; ++j)
+                            stage_quad(j, v[c + 4 * j], v[c + 4 * j + 1], v[c + 4 * j + 2], v[c + 4 * j + 3]);
+                        store_staged(row0, n0 + c);
+                    }
+                }
+            } else {
+                const int buf = n & 1;
+                if (!wait_warp(&sy.acc_full[buf], (n >> 1) & 1, abort_flag)) return;
+                ++n;
+                tc_fence_after();
+                for (int c = 0; c < half; c += STG_COLS) {
+                    uint32_t r[2][32];
+                    tmem_ld32_async(lane_acc + buf * ACC_COLS + c, r[0]);
+                    tmem_ld32_async(lane_acc + buf * ACC_COLS + c + 32, r[1]);
+                    tmem_wait_ld(r[0]);
+                    tmem_wait_ld(r[1]);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            stage_quad(k * 8 + j, __uint_as_float(r[k][4 * j]), __uint_as_float(r[k][4 * j + 1]),
+                                       __uint_as_float(r[k][4 * j + 2]), __uint_as_float(r[k][4 * j + 3]));
+                    if (c + STG_COLS >= half) release(buf);
+                    store_staged(row0, n0 + c);
+                }
+            }
+        }
+    };
+    // all products and copies done, no arrival on its way to another CTA
+    auto finish = [&]() {
+        tc_fence_before();
+        __syncthreads();
+        if (CG == 2 || SPLIT) cluster_sync();
+        tc_fence_after();
+        if (warp == 2) tmem_free<CG>(tmem);
+        if (threadIdx.x == 0 && sy.abort_flag && p.dev_status) atomicOr(p.dev_status, SC_DEV_WAIT_LIMIT);
+    };
+    // 128 sums per epilogue thread: those warps take registers over from the
+    // other four (launched with 168 each: 56 + 2 x 224 = 3 x 168).  The two
+    // sides share no code after this.
+    if constexpr (KEEP && !SPLIT) {
+        if (warp >= EPI_WARP0) {
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+            epilogue();
+            finish();
+            return;
+        }
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    }
+
+    if (warp == 0) {
+        // ================= TMA producer =================
+        if (lane == 0) {
+            Ring r = {0, 0};
+            uint32_t issued = 0;
+            bool ok = true;
+            for (int t = first_tile; t < p.n_tiles && ok; t += tile_step) {
+                const int m0 = (t / p.n_tiles_n) * (CG * GM) + rank * GM * (CG - 1);
+                const int n0 = (t % p.n_tiles_n) * p.bn + (CG == 2 ? rank * (p.bn / 2) : 0);
+                int prod = it0 / p.n_k, k = it0 % p.n_k;
+                for (int i = it0; i < it1; ++i, ++issued) {
+                    if (!mbar_wait(&sy.empty[r.slot], r.phase ^ 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t sa = base + r.slot * stage_bytes;
+                    uint32_t bar = smem_addr(&sy.full[r.slot]);
+                    if (CG == 2) bar = cluster_addr(bar, 0);
+                    if (rank == 0 || CG == 1) mbar_expect_tx(&sy.full[r.slot], CG * stage_bytes);
+                    load_tile<CG>(sa, &p.ma, bar, p.a_mn, GM, m0, k * GK, plane_a(prod, p.n_prod));
+                    load_tile<CG>(sa + A_STAGE, &p.mb, bar, p.b_mn, p.bn / CG, n0, k * GK, plane_b(prod, p.n_prod));
+                    if (++k == p.n_k) {
+                        k = 0;
+                        ++prod;
+                    }
+                    r.next(p.stages);
+                }
+            }
+            // the last copies of the ring, oldest first
+            const uint32_t last = issued < (uint32_t)p.stages ? issued : p.stages;
+            r.back(last, p.stages);
+            Ring q = r;
+            if (ok) {
+                // every stage consumed: no copy and no arrival is in flight
+                for (uint32_t j = 0; j < last; ++j, q.next(p.stages))
+                    mbar_wait(&sy.empty[q.slot], q.phase, abort_flag);
+            }
+            if (*abort_flag && (rank == 0 || CG == 1)) {
+                // gave up: let the copies that were issued land
+                int dummy = 0;
+                for (uint32_t j = 0; j < last; ++j, r.next(p.stages))
+                    mbar_wait(&sy.full[r.slot], r.phase, &dummy, WAIT_LIMIT_CYCLES / 16);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ================= MMA issuer =================
+        if (lane == 0 && (CG == 1 || rank == 0)) {
+            Ring r = {0, 0};
+            uint32_t n = 0;
+            bool ok = true;
+            for (int t = first_tile; t < p.n_tiles && ok; t += tile_step) {
+                for (int i = it0; i < it1 && ok; ++n) {
+                    const int buf = n & 1;
+                    if (!mbar_wait(&sy.acc_empty[buf], ((n >> 1) & 1) ^ 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t acc = tmem + buf * ACC_COLS;
+                    const int end = min(i + p.chunk, it1);
+                    for (bool first = true; i < end; ++i, first = false) {
+                        if (!mbar_wait(&sy.full[r.slot], r.phase, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        stage_mmas<CG>(p, acc, base + r.slot * stage_bytes, first);
+                        mma_commit<CG>(&sy.empty[r.slot]);
+                        r.next(p.stages);
+                    }
+                    if (ok) mma_commit<CG>(&sy.acc_full[buf]);
+                }
+            }
+            if (*abort_flag) {  // gave up: let the products that were issued finish
+                int dummy = 0;
+                mma_commit<1>(&sy.drain);
+                mbar_wait(&sy.drain, 0, &dummy, WAIT_LIMIT_CYCLES / 16);
+            }
+        }
+        __syncwarp();
+    } else if ((SPLIT || !KEEP) && warp >= EPI_WARP0) {
+        epilogue();
+    }
+
+    if constexpr (SPLIT) {
+        // every part is in its CTA's shared memory: add them up, a share of
+        // the rows each
+        __syncthreads();
+        cluster_sync();
+        const int parts = (int)gridDim.x / p.n_tiles;
+        const int m0 = (first_tile / p.n_tiles_n) * GM, n0 = (first_tile % p.n_tiles_n) * p.bn;
+        const int groups = p.bn / 8;
+        if (!*abort_flag) {
+            const int r0 = GM * rank / parts, r1 = GM * (rank + 1) / parts;
+            for (int i = threadIdx.x; i < (r1 - r0) * groups; i += GEMM_THREADS) {
+                const int r = r0 + i / groups, c = (i % groups) * 8;
+                if (m0 + r >= p.M || n0 + c >= p.N) continue;
+                float v[8] = {};
+                const uint32_t mine = base + (uint32_t)(r * SPLIT_LD + c) * 4;
+                for (int q = 0; q < parts; ++q) {
+                    const uint32_t at = cluster_addr(mine, q);
+                    float a[8];
+                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(a[0]), "=f"(a[1]), "=f"(a[2]), "=f"(a[3])
+                                 : "r"(at));
+                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(a[4]), "=f"(a[5]), "=f"(a[6]), "=f"(a[7])
+                                 : "r"(at + 16));
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] += a[j];
+                }
+                if (p.vec) {
+                    float b[8] = {};
+                    if (p.bias) load_any<8>(p.bias, p.bias_type, n0 + c, b);
+                    float o[1][8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) o[0][j] = v[j];
+                    epilogue_rows<ACT, 1>(p, o, b, m0 + r, 1, n0 + c);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        if (n0 + c + j >= p.N) break;
+                        float b[1] = {0.f};
+                        if (p.bias) load_any<1>(p.bias, p.bias_type, n0 + c + j, b);
+                        epilogue1<ACT>(p, v[j], b[0], m0 + r, n0 + c + j);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    }
+    finish();
+}
+
+using GemmFn = void (*)(GemmArgs);
+
+// The kernels of one activation (sc_gemm_k_*.cu).
+struct GemmKernels {
+    GemmFn pair[2], single[2];  // [result keeps fp32]
+    GemmFn split;
+};
+template <int ACT>
+GemmKernels gemm_kernels() {
+    return {{gemm_kernel<2, false, false, ACT>, gemm_kernel<2, false, true, ACT>},
+            {gemm_kernel<1, false, false, ACT>, gemm_kernel<1, false, true, ACT>},
+            gemm_kernel<1, true, true, ACT>};
+}
+GemmKernels gemm_kernels_none();
+GemmKernels gemm_kernels_relu();
+GemmKernels gemm_kernels_gelu();
+GemmKernels gemm_kernels_gelu_tanh();
+GemmKernels gemm_kernels_silu();
+
+}  // namespace gemm
+}  // namespace scb

@@ -1,0 +1,10 @@
+// The matrix product's kernels with this activation in the epilogue.
+#include "sc_gemm_dev.cuh"
+
+namespace scb {
+namespace gemm {
+
+GemmKernels gemm_kernels_relu() { return gemm_kernels<SC_ACT_RELU>(); }
+
+}  // namespace gemm
+}  // namespace scb

@@ -36,7 +36,7 @@ __device__ __forceinline__ void split3(float x, __nv_bfloat16 (&p)[3]) {
 
 // Bound by device memory.  A warp reads E columns per lane of one row at a
 // time; 8 warps of a block and gridDim.y blocks share the rows of 32 E columns.
-template <typename TIN, typename T, int E, int OUT>
+template <typename TIN, typename T, int E, int OUT, int ACT>
 __global__ void __launch_bounds__(256) pass_kernel(const PassArgs p) {
     const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
     const int64_t col = ((int64_t)blockIdx.x * 32 + lane) * E;
@@ -47,11 +47,11 @@ __global__ void __launch_bounds__(256) pass_kernel(const PassArgs p) {
         for (int64_t row = (int64_t)blockIdx.y * 8 + q; row < p.rows; row += (int64_t)gridDim.y * 8) {
             float v[E];
             load_vec<TIN, E>(static_cast<const TIN *>(p.in) + row * p.ld_in + col, v);
-            if (p.pre) {
+            if constexpr (ACT != SC_ACT_NONE) {
                 float z[E];
                 load_vec<T, E>(static_cast<const T *>(p.pre) + row * p.ld_pre + col, z);
 #pragma unroll
-                for (int e = 0; e < E; ++e) v[e] *= act_grad(z[e], p.act);
+                for (int e = 0; e < E; ++e) v[e] *= act_grad<ACT>(z[e]);
             }
 #pragma unroll
             for (int e = 0; e < E; ++e) s[e] += v[e];
@@ -97,16 +97,27 @@ int pass_chunks(int64_t rows, int64_t cols) {
     return (int)c;
 }
 
-template <typename TIN, typename T, int OUT>
+template <typename TIN, typename T, int OUT, int ACT>
 void pass(const PassArgs &p, bool vec, int chunks, cudaStream_t s) {
-    if (vec) pass_kernel<TIN, T, 8, OUT><<<dim3((unsigned)div_up(p.cols, 256), (unsigned)chunks), 256, 0, s>>>(p);
-    else pass_kernel<TIN, T, 1, OUT><<<dim3((unsigned)div_up(p.cols, 32), (unsigned)chunks), 256, 0, s>>>(p);
+    if (vec) pass_kernel<TIN, T, 8, OUT, ACT><<<dim3((unsigned)div_up(p.cols, 256), (unsigned)chunks), 256, 0, s>>>(p);
+    else pass_kernel<TIN, T, 1, OUT, ACT><<<dim3((unsigned)div_up(p.cols, 32), (unsigned)chunks), 256, 0, s>>>(p);
+}
+
+template <typename TIN, typename T, int OUT>
+void pass_act(const PassArgs &p, bool vec, int chunks, cudaStream_t s) {
+    switch (p.pre ? p.act : SC_ACT_NONE) {
+        case SC_ACT_RELU: return pass<TIN, T, OUT, SC_ACT_RELU>(p, vec, chunks, s);
+        case SC_ACT_GELU: return pass<TIN, T, OUT, SC_ACT_GELU>(p, vec, chunks, s);
+        case SC_ACT_GELU_TANH: return pass<TIN, T, OUT, SC_ACT_GELU_TANH>(p, vec, chunks, s);
+        case SC_ACT_SILU: return pass<TIN, T, OUT, SC_ACT_SILU>(p, vec, chunks, s);
+        default: return pass<TIN, T, OUT, SC_ACT_NONE>(p, vec, chunks, s);
+    }
 }
 
 template <typename TIN, typename T, int OUT>
 void pass_out(const PassArgs &p, bool vec, int chunks, cudaStream_t s) {
-    if (p.dst) pass<TIN, T, OUT>(p, vec, chunks, s);
-    else pass<TIN, T, OUT_NONE>(p, vec, chunks, s);
+    if (p.dst) pass_act<TIN, T, OUT>(p, vec, chunks, s);
+    else pass_act<TIN, T, OUT_NONE>(p, vec, chunks, s);
 }
 
 bool rows_ok(const void *p, int64_t ld, int type) { return aligned16(p) && ld * type_size(type) % 16 == 0; }
