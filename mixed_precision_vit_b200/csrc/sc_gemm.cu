@@ -95,6 +95,7 @@ int launch_gemm(int64_t M, int64_t N, int64_t K, int type16, const GemmOperand &
     p.b_mn = !b.k_major;
     p.n_tiles_n = (int)div_up(N, sh.bn);
     const int64_t tiles = div_up(M, sh.cg * GM) * p.n_tiles_n;
+    p.n_tiles_m = (int)div_up(M, sh.cg * GM);
     if (tiles > INT32_MAX / 8) {
         set_error("matrix product: %lld x %lld is too large", (long long)M, (long long)N);
         return SC_ERR_ARG;

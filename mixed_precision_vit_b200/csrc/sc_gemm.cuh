@@ -35,13 +35,54 @@ int launch_gemm(int64_t M, int64_t N, int64_t K, int type16, const GemmOperand &
 // few of exp where the result is far below |n|) stay under 2^-21 |n|.
 __device__ __forceinline__ float times_sigmoid(float n, float x) { return __fdividef(n, 1.f + __expf(-x)); }
 
+// q(a) = (1 - erf(a / sqrt 2)) / 2 for a >= 0 by the rational approximation 7.1.26 of
+// Abramowitz and Stegun, Handbook of Mathematical Functions (error below
+// 0.75e-7); it shares exp(-a^2 / 2) with gelu's derivative Phi(z) + z phi(z).
+__device__ __forceinline__ float normal_tail(float a, float e) {  // e = exp(-a^2 / 2)
+    const float t = __fdividef(1.f, 1.f + 0.231641888f * a);     // 0.3275911 / sqrt 2
+    const float s = t * (0.127414796f + t * (-0.142248368f + t * (0.7107068705f + t * (-0.7265760135f + t * 0.5307027145f))));
+    return s * e;
+}
+
 // sqrt(8 / pi) (z + 0.044715 z^3): gelu_tanh is z sigmoid of it
 __device__ __forceinline__ float gelu_tanh_arg(float z) { return 1.59576912f * z * (1.f + 0.044715f * z * z); }
+
+// Two values at a time (one packed fp32 instruction for both).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
+// gelu(z) = z Phi(z) without special functions, for the matrix product's
+// epilogue: its few warps would wait for them (16 a clock and SM).  For |z| <=
+// 5.25, Phi(z) = 1/2 + z P(z^2) with a polynomial of degree 13 in t = 2 z^2 /
+// 5.25^2 - 1 (least squares at Chebyshev nodes, weights adjusted towards equal
+// ripples: off by 0.8e-7, with fp32 roundings 1.7e-7); beyond, Phi is within
+// 0.8e-7 of 0 and 1.  The result is off by at most 4 * 2^-24 |z|.
+__device__ __forceinline__ float2 gelu2(float2 z) {
+    constexpr float A = 5.25f;
+    constexpr float P[14] = {1.346593648e-01f,  -6.712665409e-02f, 4.964389279e-02f,  -3.976862878e-02f, 3.206431866e-02f,
+                             -2.499500290e-02f, 1.832570881e-02f,  -1.295403950e-02f, 9.071036242e-03f,  -5.120746791e-03f,
+                             1.868756372e-03f,  -1.325572259e-03f, 1.456877217e-03f,  -5.612471141e-04f};
+    const float2 c = make_float2(fminf(fmaxf(z.x, -A), A), fminf(fmaxf(z.y, -A), A));
+    const float2 s = fma2(c, c, make_float2(0.f, 0.f));
+    const float2 t = fma2(s, make_float2(2.f / (A * A), 2.f / (A * A)), make_float2(-1.f, -1.f));
+    float2 h = make_float2(P[13], P[13]);
+#pragma unroll
+    for (int i = 12; i >= 0; --i) h = fma2(h, t, make_float2(P[i], P[i]));
+    const float2 f = fma2(c, h, make_float2(0.5f, 0.5f));
+    return make_float2(z.x * (z.x <= -A ? 0.f : f.x), z.y * (z.y <= -A ? 0.f : f.y));
+}
 
 template <int ACT>
 __device__ __forceinline__ float act_fn(float z) {
     if constexpr (ACT == SC_ACT_RELU) return z < 0.f ? 0.f : z;  // keeps a NaN
-    if constexpr (ACT == SC_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678f));
+    if constexpr (ACT == SC_ACT_GELU) return gelu2(make_float2(z, z)).x;
     if constexpr (ACT == SC_ACT_GELU_TANH) return times_sigmoid(z, gelu_tanh_arg(z));
     if constexpr (ACT == SC_ACT_SILU) return times_sigmoid(z, z);
     return z;
@@ -50,8 +91,11 @@ __device__ __forceinline__ float act_fn(float z) {
 template <int ACT>
 __device__ __forceinline__ float act_grad(float z) {
     if constexpr (ACT == SC_ACT_RELU) return z > 0.f ? 1.f : (z == z ? 0.f : z);
-    if constexpr (ACT == SC_ACT_GELU)
-        return 0.5f * (1.f + erff(z * 0.70710678f)) + z * 0.39894228f * __expf(-0.5f * z * z);
+    if constexpr (ACT == SC_ACT_GELU) {
+        const float a = fminf(fabsf(z), 16.f), e = __expf(-0.5f * a * a), q = normal_tail(a, e);
+        const float d = (z < 0.f ? q : 1.f - q) + (z < 0.f ? -a : a) * 0.39894228f * e;
+        return z == z ? d : z;
+    }
     if constexpr (ACT == SC_ACT_GELU_TANH) {
         const float q = times_sigmoid(1.f, gelu_tanh_arg(z));
         return q + z * q * (1.f - q) * 1.59576912f * (1.f + 0.134145f * z * z);

@@ -73,7 +73,7 @@ struct GemmArgs {
     int chunk;          // stages per accumulation
     int a_mn, b_mn;     // operand has its own index contiguous
     int bn;             // columns per tile
-    int n_tiles_n, n_tiles;
+    int n_tiles_m, n_tiles_n, n_tiles;
     int stages, b_stage, b_box_rows;
     uint32_t idesc;
     int bias_type, out_type, pre_type;
@@ -163,6 +163,17 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank) 
     return r;
 }
 
+// Row and column of tile t.  Tiles run down GROUP_M row tiles before the next
+// column, so that the tiles in work at one time share few rows and columns of
+// the operands (they stay in L2 where a whole operand does not).
+constexpr int GROUP_M = 16;
+__device__ __forceinline__ void tile_at(const GemmArgs &p, int t, int &tm, int &tn) {
+    const int per = GROUP_M * p.n_tiles_n, g = t / per, r = t - g * per;
+    const int rows = min(GROUP_M, p.n_tiles_m - g * GROUP_M);
+    tn = r / rows;
+    tm = g * GROUP_M + (r - tn * rows);
+}
+
 // The operand tile of `rows` rows (a multiple of 64 when the operand's own
 // index is contiguous) at row r0, contraction index k0.
 template <int CG>
@@ -175,15 +186,16 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap *map, 
     }
 }
 
-// Products of one stage: 4 MMAs of 16 contraction indexes.
+// Products of one stage: 4 MMAs of 16 contraction indexes.  da, db: the
+// descriptors of a stage at address 0; ka, kb: their steps.
 template <int CG>
-__device__ __forceinline__ void stage_mmas(const GemmArgs &p, uint32_t d, uint32_t sa, bool first) {
-    const uint32_t sb = sa + A_STAGE;
-    const uint32_t ka = p.a_mn ? 2048u : 32u, kb = p.b_mn ? 2048u : 32u;
+__device__ __forceinline__ void stage_mmas(uint32_t d, uint64_t da, uint64_t db, uint32_t ka, uint32_t kb,
+                                           uint32_t idesc, uint32_t sa, bool first) {
+    sa &= 0x3FFFFu;  // the offset alone: in a cluster the address also holds the CTA's rank
+    da += sa >> 4;
+    db += (sa + A_STAGE) >> 4;
 #pragma unroll
-    for (int k = 0; k < GK / 16; ++k)
-        mma_f16_ss<CG>(d, swizzled_desc(sa + k * ka, p.a_mn), swizzled_desc(sb + k * kb, p.b_mn), p.idesc,
-                       !(first && k == 0));
+    for (int k = 0; k < GK / 16; ++k) mma_f16_ss<CG>(d, da + k * ka, db + k * kb, idesc, !(first && k == 0));
 }
 
 // Epilogue of one element.
@@ -245,7 +257,16 @@ __device__ __forceinline__ void epilogue_rows(const GemmArgs &p, float (&v)[R][8
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[r][i] = act_fn<ACT>(v[r][i]);
+            for (int i = 0; i < 8; i += 2) {
+                if constexpr (ACT == SC_ACT_GELU) {
+                    const float2 g = gelu2(make_float2(v[r][i], v[r][i + 1]));
+                    v[r][i] = g.x;
+                    v[r][i + 1] = g.y;
+                } else {
+                    v[r][i] = act_fn<ACT>(v[r][i]);
+                    v[r][i + 1] = act_fn<ACT>(v[r][i + 1]);
+                }
+            }
     }
     if (p.res) {
 #pragma unroll
@@ -403,8 +424,19 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
         };
         uint32_t n = 0;
         for (int t = first_tile; t < p.n_tiles; t += tile_step) {
-            const int64_t row0 = (int64_t)(t / p.n_tiles_n) * (CG * GM) + (CG == 2 ? rank * GM : 0) + quad * 32;
-            const int n0 = (t % p.n_tiles_n) * p.bn + c_lo;
+            int tm, tn;
+            tile_at(p, t, tm, tn);
+            const int64_t row0 = (int64_t)tm * (CG * GM) + (CG == 2 ? rank * GM : 0) + quad * 32;
+            const int n0 = tn * p.bn + c_lo;
+            if (!SPLIT && p.res) {
+                // the residual's part of this tile into L2, under the products
+                const int cb = 128 / (p.out_type == SC_F32 ? 4 : 2), size = p.out_type == SC_F32 ? 4 : 2;
+                const int cols = min(half, p.N - n0);
+                if (row0 + lane < p.M)
+                    for (int c = 0; c < cols; c += cb)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char *>(p.res) +
+                                                                     ((row0 + lane) * p.ld_res + n0 + c) * size));
+            }
             const uint32_t lane_acc = tmem + c_lo + ((uint32_t)(quad * 32) << 16);
             if constexpr (KEEP) {
                 // add up the chunks: this lane's row, columns c_lo .. c_lo + half
@@ -493,8 +525,10 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
             uint32_t issued = 0;
             bool ok = true;
             for (int t = first_tile; t < p.n_tiles && ok; t += tile_step) {
-                const int m0 = (t / p.n_tiles_n) * (CG * GM) + rank * GM * (CG - 1);
-                const int n0 = (t % p.n_tiles_n) * p.bn + (CG == 2 ? rank * (p.bn / 2) : 0);
+                int tm, tn;
+                tile_at(p, t, tm, tn);
+                const int m0 = tm * (CG * GM) + (CG == 2 ? rank * GM : 0);
+                const int n0 = tn * p.bn + (CG == 2 ? rank * (p.bn / 2) : 0);
                 int prod = it0 / p.n_k, k = it0 % p.n_k;
                 for (int i = it0; i < it1; ++i, ++issued) {
                     if (!mbar_wait(&sy.empty[r.slot], r.phase ^ 1, abort_flag)) {
@@ -534,6 +568,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
     } else if (warp == 1) {
         // ================= MMA issuer =================
         if (lane == 0 && (CG == 1 || rank == 0)) {
+            const uint64_t da = swizzled_desc(0, p.a_mn), db = swizzled_desc(0, p.b_mn);
+            const uint32_t ka = (p.a_mn ? 2048u : 32u) >> 4, kb = (p.b_mn ? 2048u : 32u) >> 4;
             Ring r = {0, 0};
             uint32_t n = 0;
             bool ok = true;
@@ -553,7 +589,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
                             break;
                         }
                         tc_fence_after();
-                        stage_mmas<CG>(p, acc, base + r.slot * stage_bytes, first);
+                        stage_mmas<CG>(acc, da, db, ka, kb, p.idesc, base + r.slot * stage_bytes, first);
                         mma_commit<CG>(&sy.empty[r.slot]);
                         r.next(p.stages);
                     }
@@ -577,7 +613,9 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
         __syncthreads();
         cluster_sync();
         const int parts = (int)gridDim.x / p.n_tiles;
-        const int m0 = (first_tile / p.n_tiles_n) * GM, n0 = (first_tile % p.n_tiles_n) * p.bn;
+        int tm, tn;
+        tile_at(p, first_tile, tm, tn);
+        const int m0 = tm * GM, n0 = tn * p.bn;
         const int groups = p.bn / 8;
         if (!*abort_flag) {
             const int r0 = GM * rank / parts, r1 = GM * (rank + 1) / parts;
