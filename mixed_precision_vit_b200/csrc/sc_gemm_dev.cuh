@@ -212,47 +212,63 @@ __device__ __forceinline__ void epilogue1(const GemmArgs &p, float z, float bias
     store_any(p.out, p.out_type, row * p.ld_out + col, v[0]);
 }
 
+// 8 columns of R rows, `step` elements apart, from p on.
 template <typename T, int R>
-__device__ __forceinline__ void load_rows(const T *p, int64_t step, const bool (&in)[R], float (&v)[R][8]) {
+__device__ __forceinline__ void load_rows(const void *p, int64_t step, const bool (&in)[R], float (&v)[R][8]) {
+    const T *q = static_cast<const T *>(p);
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-        if (in[r]) load_vec<T, 8>(p + r * step, v[r]);
+    for (int r = 0; r < R; ++r, q += step)
+        if (in[r]) load_vec<T, 8>(q, v[r]);
 }
 template <typename T, int R>
-__device__ __forceinline__ void store_rows(T *p, int64_t step, const bool (&in)[R], const float (&v)[R][8]) {
+__device__ __forceinline__ void store_rows(void *p, int64_t step, const bool (&in)[R], const float (&v)[R][8]) {
+    T *q = static_cast<T *>(p);
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-        if (in[r]) store_vec<T, 8>(p + r * step, v[r]);
+    for (int r = 0; r < R; ++r, q += step)
+        if (in[r]) store_vec<T, 8>(q, v[r]);
 }
 template <int R>
-__device__ __forceinline__ void store_rows_any(void *p, int type, int64_t at, int64_t step, const bool (&in)[R],
+__device__ __forceinline__ void store_rows_any(void *p, int type, int64_t step, const bool (&in)[R],
                                                const float (&v)[R][8]) {
-    if (type == SC_F32) store_rows<float, R>(static_cast<float *>(p) + at, step, in, v);
-    else if (type == SC_BF16) store_rows<__nv_bfloat16, R>(static_cast<__nv_bfloat16 *>(p) + at, step, in, v);
-    else store_rows<__half, R>(static_cast<__half *>(p) + at, step, in, v);
+    if (type == SC_F32) store_rows<float, R>(p, step, in, v);
+    else if (type == SC_BF16) store_rows<__nv_bfloat16, R>(p, step, in, v);
+    else store_rows<__half, R>(p, step, in, v);
+}
+__device__ __forceinline__ char *at_element(const void *p, int type, int64_t i) {
+    return const_cast<char *>(static_cast<const char *>(p)) + i * (type == SC_F32 ? 4 : 2);
 }
 
-// Epilogue of columns col .. col + 7 (their bias: b) of R rows, row + i step.
-// Every step runs over all of them before the next one begins: the few warps
-// of an epilogue hide latency by independent work, not by each other.
+// Where a lane's 8 columns of a row lie in the result, and the bytes and
+// elements from there to its next rows.
+struct RowPtrs {
+    char *out, *pre;
+    const char *res;
+};
+__device__ __forceinline__ RowPtrs row_ptrs(const GemmArgs &p, int64_t row, int col) {
+    return {at_element(p.out, p.out_type, row * p.ld_out + col), at_element(p.pre, p.pre_type, row * p.ld_pre + col),
+            at_element(p.res, p.out_type, row * p.ld_res + col)};
+}
+
+// Epilogue of 8 columns (their bias: b) of R rows from q on, `step` rows apart;
+// in: the row exists.  Every step runs over all of them before the next one
+// begins: the few warps of an epilogue hide latency by independent work, not
+// by each other.
 template <int ACT, int R>
-__device__ __forceinline__ void epilogue_rows(const GemmArgs &p, float (&v)[R][8], const float (&b)[8], int64_t row,
-                                              int step, int col) {
-    bool in[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) in[r] = row + r * step < p.M;
+__device__ __forceinline__ void epilogue_rows(const GemmArgs &p, float (&v)[R][8], const float (&b)[8], const RowPtrs &q,
+                                              int step, const bool (&in)[R]) {
     float a[R][8];
     if (p.res) {
-        const int64_t at = row * p.ld_res + col, st = step * p.ld_res;
-        if (p.out_type == SC_F32) load_rows<float, R>(static_cast<const float *>(p.res) + at, st, in, a);
-        else if (p.out_type == SC_BF16) load_rows<__nv_bfloat16, R>(static_cast<const __nv_bfloat16 *>(p.res) + at, st, in, a);
-        else load_rows<__half, R>(static_cast<const __half *>(p.res) + at, st, in, a);
+        if (p.out_type == SC_F32) load_rows<float, R>(q.res, step * p.ld_res, in, a);
+        else if (p.out_type == SC_BF16) load_rows<__nv_bfloat16, R>(q.res, step * p.ld_res, in, a);
+        else load_rows<__half, R>(q.res, step * p.ld_res, in, a);
     }
+    if (p.bias) {
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+        for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[r][i] += b[i];
-    if (p.pre) store_rows_any<R>(p.pre, p.pre_type, row * p.ld_pre + col, step * p.ld_pre, in, v);
+            for (int i = 0; i < 8; ++i) v[r][i] += b[i];
+    }
+    if (p.pre) store_rows_any<R>(q.pre, p.pre_type, step * p.ld_pre, in, v);
     if constexpr (ACT != SC_ACT_NONE) {
 #pragma unroll
         for (int r = 0; r < R; ++r)
@@ -274,7 +290,7 @@ __device__ __forceinline__ void epilogue_rows(const GemmArgs &p, float (&v)[R][8
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[r][i] += a[r][i];
     }
-    store_rows_any<R>(p.out, p.out_type, row * p.ld_out + col, step * p.ld_out, in, v);
+    store_rows_any<R>(q.out, p.out_type, step * p.ld_out, in, v);
 }
 
 // tcgen05.ld without its wait; the registers are valid after tmem_wait_ld.
@@ -383,19 +399,32 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
                     float b[8] = {};
                     if (p.bias) load_any<8>(p.bias, p.bias_type, col, b);
                     constexpr int R = 4;
+                    RowPtrs q = row_ptrs(p, row0 + lr, col);
+                    const int64_t out_step = 4 * R * p.ld_out * (p.out_type == SC_F32 ? 4 : 2);
+                    const int64_t res_step = 4 * R * p.ld_res * (p.out_type == SC_F32 ? 4 : 2);
+                    const int64_t pre_step = 4 * R * p.ld_pre * (p.pre_type == SC_F32 ? 4 : 2);
+                    const int rows = (int)min((int64_t)32, p.M - row0);
+                    // the same quads for rows r and r + 8
+                    const float *s0 = stg + lr * STG_COLS + (lc ^ lr) * 4, *s1 = stg + (lr + 4) * STG_COLS + (lc ^ (lr + 4)) * 4;
 #pragma unroll 1
                     for (int r = lr; r < 32; r += 4 * R) {
                         float o[R][8];
+                        bool in[R];
 #pragma unroll
                         for (int k = 0; k < R; ++k) {
-                            const int rr = r + 4 * k;
-                            const float *q = stg + rr * STG_COLS;
-                            const float4 x = *reinterpret_cast<const float4 *>(q + (lc ^ (rr & 7)) * 4);
-                            const float4 y = *reinterpret_cast<const float4 *>(q + (8 + (lc ^ (rr & 7))) * 4);
+                            const float *f = (k & 1 ? s1 : s0) + (k >> 1) * 8 * STG_COLS;
+                            const float4 x = *reinterpret_cast<const float4 *>(f);
+                            const float4 y = *reinterpret_cast<const float4 *>(f + 32);
                             o[k][0] = x.x; o[k][1] = x.y; o[k][2] = x.z; o[k][3] = x.w;
                             o[k][4] = y.x; o[k][5] = y.y; o[k][6] = y.z; o[k][7] = y.w;
+                            in[k] = r + 4 * k < rows;
                         }
-                        epilogue_rows<ACT, R>(p, o, b, row0 + r, 4, col);
+                        epilogue_rows<ACT, R>(p, o, b, q, 4, in);
+                        s0 += 4 * R * STG_COLS;
+                        s1 += 4 * R * STG_COLS;
+                        q.out += out_step;
+                        q.res += res_step;
+                        q.pre += pre_step;
                     }
                 }
             } else {
@@ -642,7 +671,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
                     float o[1][8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) o[0][j] = v[j];
-                    epilogue_rows<ACT, 1>(p, o, b, m0 + r, 1, n0 + c);
+                    const bool in[1] = {true};
+                    epilogue_rows<ACT, 1>(p, o, b, row_ptrs(p, m0 + r, n0 + c), 0, in);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {

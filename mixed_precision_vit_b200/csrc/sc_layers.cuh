@@ -28,6 +28,33 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return
 template <>
 __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
 
+// Two 16-bit values in one word.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+template <typename T>
+__device__ __forceinline__ void unpack2(uint32_t w, float &a, float &b);
+template <>
+__device__ __forceinline__ void unpack2<__nv_bfloat16>(uint32_t w, float &a, float &b) {
+    a = __uint_as_float(w << 16);
+    b = __uint_as_float(w & 0xFFFF0000u);
+}
+template <>
+__device__ __forceinline__ void unpack2<__half>(uint32_t w, float &a, float &b) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    a = f.x;
+    b = f.y;
+}
+
 // E contiguous elements to and from fp32 registers.  E * sizeof(T) is 16 or 32
 // bytes on a 16-byte boundary, 8 bytes on an 8-byte boundary, or one element.
 template <typename T, int E>
@@ -41,14 +68,25 @@ __device__ __forceinline__ void load_vec(const T *p, float (&v)[E]) {
         uint32_t raw[B / 4];
 #pragma unroll
         for (int i = 0; i < B / 4 / W; ++i) {
-            if constexpr (W == 4)
-                reinterpret_cast<uint4 *>(raw)[i] = reinterpret_cast<const uint4 *>(p)[i];
-            else
-                reinterpret_cast<uint2 *>(raw)[i] = reinterpret_cast<const uint2 *>(p)[i];
+            if constexpr (W == 4) {
+                const uint4 q = reinterpret_cast<const uint4 *>(p)[i];
+                raw[4 * i] = q.x;
+                raw[4 * i + 1] = q.y;
+                raw[4 * i + 2] = q.z;
+                raw[4 * i + 3] = q.w;
+            } else {
+                const uint2 q = reinterpret_cast<const uint2 *>(p)[i];
+                raw[2 * i] = q.x;
+                raw[2 * i + 1] = q.y;
+            }
         }
-        const T *e = reinterpret_cast<const T *>(raw);
+        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < E; ++i) v[i] = to_f(e[i]);
+            for (int i = 0; i < E; ++i) v[i] = __uint_as_float(raw[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; i += 2) unpack2<T>(raw[i / 2], v[i], v[i + 1]);
+        }
     }
 }
 
@@ -60,15 +98,20 @@ __device__ __forceinline__ void store_vec(T *p, const float (&v)[E]) {
     } else {
         static_assert(B == 8 || B % 16 == 0, "vector width");
         constexpr int W = B == 8 ? 2 : 4;
-        alignas(16) T e[E];
+        uint32_t e[B / 4];
+        if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < E; ++i) e[i] = from_f<T>(v[i]);
+            for (int i = 0; i < E; ++i) e[i] = __float_as_uint(v[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; i += 2) e[i / 2] = pack2<T>(v[i], v[i + 1]);
+        }
 #pragma unroll
         for (int i = 0; i < B / 4 / W; ++i) {
             if constexpr (W == 4)
-                reinterpret_cast<uint4 *>(p)[i] = reinterpret_cast<const uint4 *>(e)[i];
+                reinterpret_cast<uint4 *>(p)[i] = make_uint4(e[4 * i], e[4 * i + 1], e[4 * i + 2], e[4 * i + 3]);
             else
-                reinterpret_cast<uint2 *>(p)[i] = reinterpret_cast<const uint2 *>(e)[i];
+                reinterpret_cast<uint2 *>(p)[i] = make_uint2(e[2 * i], e[2 * i + 1]);
         }
     }
 }
