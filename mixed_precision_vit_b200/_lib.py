@@ -130,9 +130,17 @@ def load():
         return lib
 
 
-def _check(code: int):
+def lib():
+    """The loaded library, loading it on the first call."""
+    return _lib if _lib is not None else load()
+
+
+def check(code: int):
     if code != SC_OK:
         raise ScError(code, load().sc_last_error().decode())
+
+
+_check = check
 
 
 def _ptr(x):
@@ -302,7 +310,7 @@ def sc_layer_norm_backward(desc: ScNormDesc, dy, x, weight, mean, rstd, dx_add, 
 
 
 def sc_layer_norm_workspace_bytes(desc: ScNormDesc) -> int:
-    return _bytes(load().sc_layer_norm_workspace_bytes(ctypes.byref(desc)))
+    return check_bytes(load().sc_layer_norm_workspace_bytes(ctypes.byref(desc)))
 
 
 def sc_linear(desc: ScLinearDesc, x, w, bias, residual, out, pre, dev_status, stream=None):
@@ -317,15 +325,16 @@ def sc_linear_backward(desc: ScLinearDesc, dout, x, w, pre, dx, dw, dbias, dev_s
 
 
 def sc_linear_workspace_bytes(desc: ScLinearDesc, x, w) -> int:
-    return _bytes(load().sc_linear_workspace_bytes(ctypes.byref(desc), _ptr(x), _ptr(w)))
+    return check_bytes(load().sc_linear_workspace_bytes(ctypes.byref(desc), _ptr(x), _ptr(w)))
 
 
 def sc_linear_backward_workspace_bytes(desc: ScLinearDesc, dout, x, w) -> int:
-    return _bytes(load().sc_linear_backward_workspace_bytes(ctypes.byref(desc), _ptr(dout), _ptr(x),
+    return check_bytes(load().sc_linear_backward_workspace_bytes(ctypes.byref(desc), _ptr(dout), _ptr(x),
                                                             _ptr(w)))
 
 
-def _bytes(n: int) -> int:
+def check_bytes(n: int) -> int:
+    """A byte count, or minus a status."""
     if n < 0:
-        _check(-n)
+        check(-n)
     return n

@@ -199,25 +199,21 @@ def _type(dtype, what: str) -> int:
         raise ValueError(f"{what} must be float32, bfloat16 or float16, not {dtype}") from None
 
 
-def _matrix(t: torch.Tensor, what: str, like: torch.Tensor = None, shape=None, dtype=None):
+def _matrix(t: torch.Tensor, what: str):
     """(rows, columns, row stride) of a [..., columns] CUDA tensor."""
     if not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
-    if like is not None and t.device != like.device:
-        raise ValueError(f"{what} is on {t.device}, not on {like.device}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{what} must be {dtype}, not {t.dtype}")
-    if t.dim() == 0:
+    shape = t.shape
+    if not shape:
         raise ValueError(f"{what} must have at least one dimension")
-    cols = t.shape[-1]
+    cols = shape[-1]
     if t.is_contiguous():
-        return (t.numel() // cols if cols else 0), cols, cols
-    if cols > 1 and t.stride(-1) != 1:
+        return (shape[0] if len(shape) == 2 else t.numel() // cols if cols else 0), cols, cols
+    strides = t.stride()
+    if cols > 1 and strides[-1] != 1:
         raise ValueError(f"{what}: elements of a row must be contiguous")
     rows, ld = 1, None
-    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+    for n, st in zip(reversed(shape[:-1]), reversed(strides[:-1])):
         if n == 1:
             continue
         if ld is None:
@@ -231,17 +227,32 @@ def _matrix(t: torch.Tensor, what: str, like: torch.Tensor = None, shape=None, d
     return rows, cols, ld
 
 
-def _vector(t, n: int, what: str, like: torch.Tensor, dtype=None):
-    if t is None:
-        return
-    if t.device != like.device or not t.is_contiguous() or t.shape != (n,):
-        raise ValueError(f"{what} must be a contiguous [{n}] tensor on {like.device}")
+def _like(t: torch.Tensor, what: str, dev: int, shape, dtype=None) -> int:
+    """Row stride of a matrix that must have this shape, type and device."""
+    ld = _matrix(t, what)[2]
+    if t.get_device() != dev:
+        raise ValueError(f"{what} is on {t.device}, not on device {dev}")
+    if t.shape != shape:
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}, not {t.dtype}")
+    return ld
+
+
+def _vector(t: torch.Tensor, n: int, what: str, dev: int, dtype=None):
+    if t.get_device() != dev or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous [{n}] tensor on device {dev}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{what} must be {dtype}, not {t.dtype}")
 
 
-def _elsewhere(t: torch.Tensor, stream) -> bool:
-    return stream is not None or t.device.index != torch.cuda.current_device()
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+# the current stream's handle (torch.cuda.current_stream costs more than a launch)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 class _On:
@@ -280,9 +291,10 @@ def _scratch(desc, need: int, workspace, like: torch.Tensor):
 
 def _act_code(act) -> int:
     if isinstance(act, str):
-        if act not in ACTIVATIONS:
-            raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, not {act!r}")
-        return ACTIVATIONS[act]
+        try:
+            return ACTIVATIONS[act]
+        except KeyError:
+            raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, not {act!r}") from None
     return int(act)
 
 
@@ -295,20 +307,32 @@ def layer_norm(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-6, *, ou
     (fp32, x.shape[:-1]) are returned with want_stats, for layer_norm_backward, and are
     None otherwise.  out: the tensor to write, which may be x itself (same type)."""
     rows, D, ld = _matrix(x, "x")
-    if _elsewhere(x, stream):
+    dev = x.get_device()
+    if stream is not None or dev != torch.cuda.current_device():
         with _On(x.device, stream):
             return layer_norm(x, weight, bias, eps, out_dtype=out_dtype, want_stats=want_stats, out=out)
-    _vector(weight, D, "weight", x)
-    _vector(bias, D, "bias", x, None if weight is None else weight.dtype)
+    xt = x.dtype
+    shape = x.shape
+    wt = L.SC_F32
+    if bias is not None:
+        _vector(bias, D, "bias", dev, None if weight is None else weight.dtype)
+        wt = _type(bias.dtype, "bias")
+    if weight is not None:
+        _vector(weight, D, "weight", dev)
+        wt = _type(weight.dtype, "weight")
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
-    _, _, ld_y = _matrix(out, "out", x, x.shape, out_dtype)
-    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if want_stats else None
-    rstd = torch.empty_like(mean) if want_stats else None
-    p = weight if weight is not None else bias
-    d = L.ScNormDesc(rows, D, ld, ld_y, 0, 0, eps, _type(x.dtype, "x"), _type(out.dtype, "out"),
-                     L.SC_F32 if p is None else _type(p.dtype, "weight and bias"))
-    L.sc_layer_norm(d, x, weight, bias, out, mean, rstd, torch.cuda.current_stream())
+        out = x.new_empty(shape, dtype=out_dtype or xt)
+        ld_y = D
+    else:
+        ld_y = _like(out, "out", dev, shape, out_dtype)
+    mean = rstd = None
+    if want_stats:
+        lead = (rows,) if len(shape) == 2 else shape[:-1]
+        mean = x.new_empty(lead, dtype=torch.float32)
+        rstd = x.new_empty(lead, dtype=torch.float32)
+    d = L.ScNormDesc(rows, D, ld, ld_y, 0, 0, eps, _type(xt, "x"), _type(out.dtype, "out"), wt)
+    L.check(L.lib().sc_layer_norm(d, x.data_ptr(), _ptr(weight), _ptr(bias), out.data_ptr(),
+                                  _ptr(mean), _ptr(rstd), _raw_stream(dev)))
     return out, mean, rstd
 
 
@@ -323,32 +347,41 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
     default when there is a weight, and are None otherwise.  workspace: device scratch
     of sc_layer_norm_workspace_bytes, allocated when None."""
     rows, D, ld = _matrix(x, "x")
-    if _elsewhere(x, stream):
+    dev = x.get_device()
+    if stream is not None or dev != torch.cuda.current_device():
         with _On(x.device, stream):
             return layer_norm_backward(dy, x, mean, rstd, weight, dx_add=dx_add, want_dx=want_dx,
                                        want_params=want_params, param_dtype=param_dtype,
                                        workspace=workspace)
-    _, _, ld_y = _matrix(dy, "dy", x, x.shape)
+    xt = x.dtype
+    shape = x.shape
+    ld_y = _like(dy, "dy", dev, shape)
     for t, what in ((mean, "mean"), (rstd, "rstd")):
-        if t.dtype != torch.float32 or t.device != x.device or t.numel() != rows or not t.is_contiguous():
-            raise ValueError(f"{what} must be a contiguous float32 tensor of {rows} values on {x.device}")
-    _vector(weight, D, "weight", x)
-    if want_params is None:
-        want_params = weight is not None
-    if weight is not None and param_dtype is not None and param_dtype != weight.dtype:
-        raise ValueError("dweight and dbias have the weight's type")
-    pt = weight.dtype if weight is not None else (param_dtype or torch.float32)
-    ld_add = 0
-    if dx_add is not None:
-        _, _, ld_add = _matrix(dx_add, "dx_add", x, x.shape, x.dtype)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if want_dx else None
-    dw = torch.empty(D, dtype=pt, device=x.device) if want_params else None
-    db = torch.empty_like(dw) if want_params else None
-    d = L.ScNormDesc(rows, D, ld, ld_y, D, ld_add, 0.0, _type(x.dtype, "x"), _type(dy.dtype, "dy"),
+        if t.dtype != torch.float32 or t.get_device() != dev or t.numel() != rows or not t.is_contiguous():
+            raise ValueError(f"{what} must be a contiguous float32 tensor of {rows} values on device {dev}")
+    if weight is not None:
+        _vector(weight, D, "weight", dev)
+        if param_dtype is not None and param_dtype != weight.dtype:
+            raise ValueError("dweight and dbias have the weight's type")
+        pt = weight.dtype
+        if want_params is None:
+            want_params = True
+    else:
+        pt = param_dtype or torch.float32
+    ld_add = 0 if dx_add is None else _like(dx_add, "dx_add", dev, shape, xt)
+    dx = x.new_empty(shape) if want_dx else None
+    dw = db = None
+    d = L.ScNormDesc(rows, D, ld, ld_y, D, ld_add, 0.0, _type(xt, "x"), _type(dy.dtype, "dy"),
                      _type(pt, "weight"))
-    ws = _scratch(d, L.sc_layer_norm_workspace_bytes(d) if want_params else 0, workspace, x)
-    L.sc_layer_norm_backward(d, dy, x, weight, mean, rstd, dx_add, dx, dw, db,
-                             torch.cuda.current_stream())
+    lib = L.lib()
+    ws = None
+    if want_params:
+        dw = x.new_empty((D,), dtype=pt)
+        db = x.new_empty((D,), dtype=pt)
+        ws = _scratch(d, L.check_bytes(lib.sc_layer_norm_workspace_bytes(d)), workspace, x)
+    L.check(lib.sc_layer_norm_backward(d, dy.data_ptr(), x.data_ptr(), _ptr(weight), mean.data_ptr(),
+                                       rstd.data_ptr(), _ptr(dx_add), _ptr(dx), _ptr(dw), _ptr(db),
+                                       _raw_stream(dev)))
     del ws
     return dx, dw, db
 
@@ -361,30 +394,39 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias=None, residual=None, act="none
     are, fp32 as three bf16 parts); bias [N] of any type; residual and out [..., N] of
     out_dtype, which is x's type (default) or float32.  act: a key of ACTIVATIONS.  pre
     is x w^T + bias in x's type with want_pre (what linear_backward needs for an
-    activation), else None.  out: the tensor to write, which may be the residual."""
+    activation), else None.  out: the tensor to write, which may be the residual.
+    workspace: device scratch of sc_linear_workspace_bytes, allocated when None."""
     M, K, ld_x = _matrix(x, "x")
-    if _elsewhere(x, stream):
+    dev = x.get_device()
+    if stream is not None or dev != torch.cuda.current_device():
         with _On(x.device, stream):
             return linear(x, w, bias, residual, act, out_dtype=out_dtype, want_pre=want_pre, out=out,
                           workspace=workspace, dev_status=dev_status)
+    xt = x.dtype
+    ot = out_dtype or xt
     if w.dim() != 2:
         raise ValueError(f"w has shape {tuple(w.shape)}, not [N, {K}]")
     N = w.shape[0]
-    _, _, ld_w = _matrix(w, "w", x, (N, K), x.dtype)
-    _vector(bias, N, "bias", x)
-    shape = x.shape[:-1] + (N,)
-    ld_res = 0
-    if residual is not None:
-        _, _, ld_res = _matrix(residual, "residual", x, shape, out_dtype or x.dtype)
+    ld_w = _like(w, "w", dev, (N, K), xt)
+    bt = L.SC_F32
+    if bias is not None:
+        _vector(bias, N, "bias", dev)
+        bt = _type(bias.dtype, "bias")
+    shape = (M, N) if x.dim() == 2 else x.shape[:-1] + (N,)
+    ld_res = 0 if residual is None else _like(residual, "residual", dev, shape, ot)
+    ld_out = N
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype or x.dtype, device=x.device)
-    _, _, ld_out = _matrix(out, "out", x, shape, out_dtype or x.dtype)
-    pre = torch.empty(shape, dtype=x.dtype, device=x.device) if want_pre else None
-    d = L.ScLinearDesc(M, N, K, ld_x, ld_w, ld_out, ld_res, N, 0, 0, _type(x.dtype, "x"),
-                       _type(out.dtype, "out"),
-                       L.SC_F32 if bias is None else _type(bias.dtype, "bias"), 0, _act_code(act))
-    ws = _scratch(d, L.sc_linear_workspace_bytes(d, x, w), workspace, x)
-    L.sc_linear(d, x, w, bias, residual, out, pre, dev_status, torch.cuda.current_stream())
+        out = x.new_empty(shape, dtype=ot)
+    else:
+        ld_out = _like(out, "out", dev, shape, ot)
+    pre = x.new_empty(shape) if want_pre else None
+    d = L.ScLinearDesc(M, N, K, ld_x, ld_w, ld_out, ld_res, N, 0, 0, _type(xt, "x"), _type(ot, "out"),
+                       bt, 0, _act_code(act))
+    lib = L.lib()
+    xp, wp = x.data_ptr(), w.data_ptr()
+    ws = _scratch(d, L.check_bytes(lib.sc_linear_workspace_bytes(d, xp, wp)), workspace, x)
+    L.check(lib.sc_linear(d, xp, wp, _ptr(bias), _ptr(residual), out.data_ptr(), _ptr(pre),
+                          _ptr(dev_status), _raw_stream(dev)))
     del ws
     return out, pre
 
@@ -396,34 +438,39 @@ def linear_backward(dout: torch.Tensor, x: torch.Tensor, w: torch.Tensor, pre=No
 
     dout [..., N] of x's type or float32; pre as linear returned it (needed with an
     activation).  dx has x's type, dw and db grad_dtype (w's type by default).  The
-    residual's gradient is dout itself."""
+    residual's gradient is dout itself.  workspace: device scratch of
+    sc_linear_backward_workspace_bytes, allocated when None."""
     M, K, ld_x = _matrix(x, "x")
-    if _elsewhere(x, stream):
+    dev = x.get_device()
+    if stream is not None or dev != torch.cuda.current_device():
         with _On(x.device, stream):
             return linear_backward(dout, x, w, pre, act, want_dx=want_dx, want_dw=want_dw,
                                    want_db=want_db, grad_dtype=grad_dtype, workspace=workspace,
                                    dev_status=dev_status)
+    xt = x.dtype
     if w.dim() != 2:
         raise ValueError(f"w has shape {tuple(w.shape)}, not [N, {K}]")
     N = w.shape[0]
-    _, _, ld_w = _matrix(w, "w", x, (N, K), x.dtype)
-    shape = x.shape[:-1] + (N,)
-    _, _, ld_out = _matrix(dout, "dout", x, shape)
+    ld_w = _like(w, "w", dev, (N, K), xt)
+    shape = (M, N) if x.dim() == 2 else x.shape[:-1] + (N,)
+    ld_out = _like(dout, "dout", dev, shape)
     code = _act_code(act)
     ld_pre = 0
     if code != L.SC_ACT_NONE:
         if pre is None:
             raise ValueError("an activation's gradient needs pre")
-        _, _, ld_pre = _matrix(pre, "pre", x, shape, x.dtype)
-    gt = grad_dtype or w.dtype
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if want_dx else None
-    dw = torch.empty(N, K, dtype=gt, device=x.device) if want_dw else None
-    db = torch.empty(N, dtype=gt, device=x.device) if want_db else None
-    d = L.ScLinearDesc(M, N, K, ld_x, ld_w, ld_out, 0, ld_pre, K, K, _type(x.dtype, "x"),
+        ld_pre = _like(pre, "pre", dev, shape, xt)
+    gt = grad_dtype or xt
+    dx = x.new_empty(x.shape) if want_dx else None
+    dw = x.new_empty((N, K), dtype=gt) if want_dw else None
+    db = x.new_empty((N,), dtype=gt) if want_db else None
+    d = L.ScLinearDesc(M, N, K, ld_x, ld_w, ld_out, 0, ld_pre, K, K, _type(xt, "x"),
                        _type(dout.dtype, "dout"), 0, _type(gt, "grad_dtype"), code)
-    ws = _scratch(d, L.sc_linear_backward_workspace_bytes(d, dout, x, w), workspace, x)
-    L.sc_linear_backward(d, dout, x, w, pre if code else None, dx, dw, db, dev_status,
-                         torch.cuda.current_stream())
+    lib = L.lib()
+    dp, xp, wp = dout.data_ptr(), x.data_ptr(), w.data_ptr()
+    ws = _scratch(d, L.check_bytes(lib.sc_linear_backward_workspace_bytes(d, dp, xp, wp)), workspace, x)
+    L.check(lib.sc_linear_backward(d, dp, xp, wp, _ptr(pre) if code else None, _ptr(dx), _ptr(dw),
+                                   _ptr(db), _ptr(dev_status), _raw_stream(dev)))
     del ws
     return dx, dw, db
 
