@@ -1,6 +1,7 @@
 // sc_gemm.cu -- host side of the matrix product: tensor maps, tile shapes and
 // launches of the kernels in sc_gemm_dev.cuh.
 #include "sc_gemm_dev.cuh"
+#include <atomic>
 
 namespace scb {
 namespace {
@@ -63,20 +64,69 @@ int launch(GemmFn kern, const GemmArgs &p, int grid, int cluster, cudaStream_t s
     return e == cudaSuccess ? SC_OK : cuda_fail(e, "matrix product");
 }
 
+// Clusters of `parts` CTAs of the split kernel that fit the device at one
+// time (asked once per device and size; fewer than SMs / parts, since a
+// cluster stays within one GPC).
+int split_clusters(int parts) {
+    constexpr int DEVICES = 64;
+    static std::atomic<int> known[DEVICES][MAX_PARTS + 1];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= DEVICES) return sm_count() / (2 * parts);
+    int n = known[dev][parts].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    const GemmFn kern = gemm_kernels_none().split;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = parts;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(parts * sm_count()));
+    cfg.blockDim = dim3(GEMM_THREADS);
+    cfg.dynamicSmemBytes = GEMM_SMEM;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GEMM_SMEM) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        return sm_count() / (2 * parts);
+    }
+    known[dev][parts].store(n, std::memory_order_relaxed);
+    return n;
+}
+
 struct Shape {
     int cg, bn, parts;
 };
 
-// Tile shape: 256 x 256 by CTA pairs when that fills the SMs, else 128-row
-// tiles, else tiles whose contraction several CTAs share.
+// The tile shape with the least estimated time.  Measured (us, bf16): a stage
+// of 64 indexes costs 0.30 in a pair's 256 x 256 tile and 0.24 in a CTA's 128 x
+// 128 tile or less (there the issuing threads, not the products, set the pace);
+// a launch 6.0 or 5.0 besides; parts of a shared tile cost their exchange,
+// 0.005 per column and part.  So 4112 x 1024 x 4096 takes 25.5 in pairs
+// (68 tiles, one round) and 37.2 in single CTAs (264 tiles, two rounds); 2056 x
+// 1024 x 1024 takes 10.6 and 8.5; 257 x 1024 x 4096 takes 13.0 in 4 parts of
+// 128 columns and 28 unshared.
 Shape choose(int64_t M, int64_t N, int n_it) {
     const int sms = sm_count();
-    const int64_t t2 = div_up(M, 256) * div_up(N, 256);
-    if (2 * t2 >= sms) return {2, 256, 1};
-    const int64_t t1 = div_up(M, 128) * div_up(N, 128);
-    int parts = 1;
-    while (parts < 8 && t1 * parts * 2 <= sms && n_it >= 4 * parts) parts *= 2;
-    return {1, 128, parts};
+    auto rounds = [](int64_t tiles, int units) { return (double)div_up(tiles, units < 1 ? 1 : units); };
+    const int64_t rows = div_up(M, GM);
+    Shape best = {2, 256, 1};
+    double least = 6.0 + 0.30 * n_it * rounds(div_up(M, 2 * GM) * div_up(N, 256), sms / 2);
+    auto consider = [&](const Shape &s, double t) {
+        if (t < least) {
+            least = t;
+            best = s;
+        }
+    };
+    consider({1, 128, 1}, 5.0 + 0.24 * n_it * rounds(rows * div_up(N, 128), sms));
+    for (int bn = 64; bn <= SPLIT_N; bn *= 2) {
+        const int64_t tiles = rows * div_up(N, bn);
+        for (int parts = 2; parts <= MAX_PARTS && 2 * parts <= n_it && tiles * parts <= sms; ++parts)
+            if (tiles <= split_clusters(parts))
+                consider({1, bn, parts}, 5.0 + 0.008 * bn + 0.005 * bn * parts + 0.24 * (double)div_up(n_it, parts));
+    }
+    return best;
 }
 
 }  // namespace

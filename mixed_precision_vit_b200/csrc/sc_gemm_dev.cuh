@@ -59,6 +59,7 @@ constexpr int ACC_COLS = 256;           // tensor-memory columns per accumulator
 constexpr int GN_MAX = 256;            // columns per tile
 constexpr int SPLIT_N = 128;            // columns of a tile whose contraction is shared
 constexpr int SPLIT_LD = SPLIT_N + 4;
+constexpr int MAX_PARTS = 8;            // the portable cluster size
 static_assert(GM * SPLIT_LD * 4 <= RING_BYTES, "parts of a shared tile fit the ring");
 
 struct GemmArgs {
@@ -155,6 +156,13 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, u
             "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
             "l"(map), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
             : "memory");
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 __device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank) {
@@ -344,7 +352,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
     uint8_t *ring = smem_raw + (base - smem_addr(smem_raw));
     GemmSync &sy = *reinterpret_cast<GemmSync *>(ring + RING_BYTES + EPI_WARPS * STG_BYTES);
     volatile int *abort_flag = &sy.abort_flag;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = CG == 2 || SPLIT ? (int)cluster_rank() : 0;
     const int first_tile = CG == 2 || SPLIT ? (int)cluster_id() : (int)blockIdx.x;
     const int tile_step = SPLIT ? p.n_tiles : CG == 2 ? (int)cluster_count() : (int)gridDim.x;
@@ -549,54 +557,56 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
 
     if (warp == 0) {
         // ================= TMA producer =================
-        if (lane == 0) {
-            Ring r = {0, 0};
-            uint32_t issued = 0;
-            bool ok = true;
-            for (int t = first_tile; t < p.n_tiles && ok; t += tile_step) {
-                int tm, tn;
-                tile_at(p, t, tm, tn);
-                const int m0 = tm * (CG * GM) + (CG == 2 ? rank * GM : 0);
-                const int n0 = tn * p.bn + (CG == 2 ? rank * (p.bn / 2) : 0);
-                int prod = it0 / p.n_k, k = it0 % p.n_k;
-                for (int i = it0; i < it1; ++i, ++issued) {
-                    if (!mbar_wait(&sy.empty[r.slot], r.phase ^ 1, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t sa = base + r.slot * stage_bytes;
-                    uint32_t bar = smem_addr(&sy.full[r.slot]);
-                    if (CG == 2) bar = cluster_addr(bar, 0);
+        // This warp and the next walk their loops as a whole, with one elected
+        // lane issuing: descriptors, addresses and coordinates then live in
+        // uniform registers, which the issued instructions take (a lone thread
+        // moves them there for every instruction: 380 cycles a stage).
+        Ring r = {0, 0};
+        uint32_t issued = 0;
+        bool ok = true;
+        const uint32_t full0 = CG == 2 ? cluster_addr(smem_addr(&sy.full[0]), 0) : smem_addr(&sy.full[0]);
+        for (int t = first_tile; t < p.n_tiles && ok; t += tile_step) {
+            int tm, tn;
+            tile_at(p, t, tm, tn);
+            const int m0 = tm * (CG * GM) + (CG == 2 ? rank * GM : 0);
+            const int n0 = tn * p.bn + (CG == 2 ? rank * (p.bn / 2) : 0);
+            int prod = it0 / p.n_k, k = it0 % p.n_k;
+            for (int i = it0; i < it1; ++i, ++issued) {
+                if (!wait_warp(&sy.empty[r.slot], r.phase ^ 1, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                if (elect_one()) {
+                    const uint32_t sa = base + r.slot * stage_bytes, bar = full0 + r.slot * 8;
                     if (rank == 0 || CG == 1) mbar_expect_tx(&sy.full[r.slot], CG * stage_bytes);
                     load_tile<CG>(sa, &p.ma, bar, p.a_mn, GM, m0, k * GK, plane_a(prod, p.n_prod));
                     load_tile<CG>(sa + A_STAGE, &p.mb, bar, p.b_mn, p.bn / CG, n0, k * GK, plane_b(prod, p.n_prod));
-                    if (++k == p.n_k) {
-                        k = 0;
-                        ++prod;
-                    }
-                    r.next(p.stages);
                 }
+                if (++k == p.n_k) {
+                    k = 0;
+                    ++prod;
+                }
+                r.next(p.stages);
             }
-            // the last copies of the ring, oldest first
-            const uint32_t last = issued < (uint32_t)p.stages ? issued : p.stages;
-            r.back(last, p.stages);
-            Ring q = r;
-            if (ok) {
-                // every stage consumed: no copy and no arrival is in flight
-                for (uint32_t j = 0; j < last; ++j, q.next(p.stages))
-                    mbar_wait(&sy.empty[q.slot], q.phase, abort_flag);
-            }
-            if (*abort_flag && (rank == 0 || CG == 1)) {
-                // gave up: let the copies that were issued land
-                int dummy = 0;
-                for (uint32_t j = 0; j < last; ++j, r.next(p.stages))
-                    mbar_wait(&sy.full[r.slot], r.phase, &dummy, WAIT_LIMIT_CYCLES / 16);
-            }
+        }
+        // the last copies of the ring, oldest first
+        const uint32_t last = issued < (uint32_t)p.stages ? issued : p.stages;
+        r.back(last, p.stages);
+        Ring q = r;
+        if (ok) {
+            // every stage consumed: no copy and no arrival is in flight
+            for (uint32_t j = 0; j < last; ++j, q.next(p.stages)) wait_warp(&sy.empty[q.slot], q.phase, abort_flag);
+        }
+        if (*abort_flag && (rank == 0 || CG == 1)) {
+            // gave up: let the copies that were issued land
+            int dummy = 0;
+            for (uint32_t j = 0; j < last; ++j, r.next(p.stages))
+                mbar_wait(&sy.full[r.slot], r.phase, &dummy, WAIT_LIMIT_CYCLES / 16);
         }
         __syncwarp();
     } else if (warp == 1) {
         // ================= MMA issuer =================
-        if (lane == 0 && (CG == 1 || rank == 0)) {
+        if (CG == 1 || rank == 0) {
             const uint64_t da = swizzled_desc(0, p.a_mn), db = swizzled_desc(0, p.b_mn);
             const uint32_t ka = (p.a_mn ? 2048u : 32u) >> 4, kb = (p.b_mn ? 2048u : 32u) >> 4;
             Ring r = {0, 0};
@@ -605,7 +615,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
             for (int t = first_tile; t < p.n_tiles && ok; t += tile_step) {
                 for (int i = it0; i < it1 && ok; ++n) {
                     const int buf = n & 1;
-                    if (!mbar_wait(&sy.acc_empty[buf], ((n >> 1) & 1) ^ 1, abort_flag)) {
+                    if (!wait_warp(&sy.acc_empty[buf], ((n >> 1) & 1) ^ 1, abort_flag)) {
                         ok = false;
                         break;
                     }
@@ -613,21 +623,23 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
                     const uint32_t acc = tmem + buf * ACC_COLS;
                     const int end = min(i + p.chunk, it1);
                     for (bool first = true; i < end; ++i, first = false) {
-                        if (!mbar_wait(&sy.full[r.slot], r.phase, abort_flag)) {
+                        if (!wait_warp(&sy.full[r.slot], r.phase, abort_flag)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        stage_mmas<CG>(acc, da, db, ka, kb, p.idesc, base + r.slot * stage_bytes, first);
-                        mma_commit<CG>(&sy.empty[r.slot]);
+                        if (elect_one()) {
+                            stage_mmas<CG>(acc, da, db, ka, kb, p.idesc, base + r.slot * stage_bytes, first);
+                            mma_commit<CG>(&sy.empty[r.slot]);
+                            if (i + 1 == end) mma_commit<CG>(&sy.acc_full[buf]);
+                        }
                         r.next(p.stages);
                     }
-                    if (ok) mma_commit<CG>(&sy.acc_full[buf]);
                 }
             }
             if (*abort_flag) {  // gave up: let the products that were issued finish
                 int dummy = 0;
-                mma_commit<1>(&sy.drain);
+                if (elect_one()) mma_commit<1>(&sy.drain);
                 mbar_wait(&sy.drain, 0, &dummy, WAIT_LIMIT_CYCLES / 16);
             }
         }
