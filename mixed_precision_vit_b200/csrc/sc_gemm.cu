@@ -44,21 +44,32 @@ bool encode(CUtensorMap *map, int type16, const GemmOperand &o, int64_t rows, in
 // 8 columns per access: rows on 16-byte boundaries
 bool vec_rows(const void *p, int64_t ld, int type) { return aligned16(p) && ld * type_size(type) % 16 == 0; }
 
-int launch(GemmFn kern, const GemmArgs &p, int grid, int cluster, cudaStream_t stream) {
+// early: may start before the previous kernel on the stream has ended (the
+// kernel itself waits for it, see GemmAfter).
+int launch(GemmFn kern, const GemmArgs &p, int grid, int cluster, bool early, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GEMM_SMEM);
     if (e != cudaSuccess) return cuda_fail(e, "matrix product: smem attribute");
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cluster;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = cluster;
+        attr[n].val.clusterDim.y = 1;
+        attr[n].val.clusterDim.z = 1;
+        ++n;
+    }
+    if (early) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n].val.programmaticStreamSerializationAllowed = 1;
+        ++n;
+    }
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(GEMM_THREADS);
     cfg.dynamicSmemBytes = GEMM_SMEM;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    cfg.numAttrs = n;
     e = cudaLaunchKernelEx(&cfg, kern, p);
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? SC_OK : cuda_fail(e, "matrix product");
@@ -132,7 +143,8 @@ Shape choose(int64_t M, int64_t N, int n_it) {
 }  // namespace
 
 int launch_gemm(int64_t M, int64_t N, int64_t K, int type16, const GemmOperand &a, const GemmOperand &b,
-                const GemmEpilogue &epi, int32_t *dev_status, cudaStream_t stream) {
+                const GemmEpilogue &epi, GemmAfter after, const ColumnSums *sums, int32_t *dev_status,
+                cudaStream_t stream) {
     GemmArgs p;
     p.n_prod = a.planes == 3 ? 6 : 1;
     p.n_k = (int)div_up(K, GK);
@@ -171,6 +183,9 @@ int launch_gemm(int64_t M, int64_t N, int64_t K, int type16, const GemmOperand &
     p.vec = N % 8 == 0 && vec_rows(epi.out, epi.ld_out, epi.out_type) &&
             (!epi.res || vec_rows(epi.res, epi.ld_res, epi.out_type)) &&
             (!epi.pre || vec_rows(epi.pre, epi.ld_pre, epi.pre_type)) && aligned16(epi.bias);
+    p.sums = sums ? *sums : ColumnSums{};
+    p.beside = after == BESIDE_GEMM;
+    const bool early = after != AFTER_ANY;
     p.dev_status = dev_status;
     if (!encode(&p.ma, type16, a, M, K, GM) || !encode(&p.mb, type16, b, N, K, sh.bn / sh.cg)) {
         set_error("matrix product: the tensor map was rejected");
@@ -184,10 +199,10 @@ int launch_gemm(int64_t M, int64_t N, int64_t K, int type16, const GemmOperand &
         case SC_ACT_SILU: k = gemm_kernels_silu(); break;
         default: k = gemm_kernels_none(); break;
     }
-    if (sh.parts > 1) return launch(k.split, p, p.n_tiles * sh.parts, sh.parts, stream);
+    if (sh.parts > 1) return launch(k.split, p, p.n_tiles * sh.parts, sh.parts, early, stream);
     const int units = sm_count() / sh.cg;
     return launch((sh.cg == 2 ? k.pair : k.single)[epi.out_type == SC_F32], p,
-                  sh.cg * (p.n_tiles < units ? p.n_tiles : units), sh.cg, stream);
+                  sh.cg * (p.n_tiles < units ? p.n_tiles : units), sh.cg, early, stream);
 }
 
 }  // namespace scb

@@ -26,9 +26,25 @@ struct GemmEpilogue {
     int bias_type, out_type, pre_type, act;
 };
 
+// Column sums left to finish: out[c] = sum_i part[i][c], i < n, in ascending i.
+struct ColumnSums {
+    const float *part;
+    void *out;
+    int64_t cols;
+    int n, type;
+};
+
+// What the launch follows on its stream, within the same call.
+enum GemmAfter {
+    AFTER_ANY,    // anything: starts when all earlier work is done
+    AFTER_PASS,   // a pass that makes its operands: sets itself up under it
+    BESIDE_GEMM,  // another product of the same passes: runs on the SMs which that one leaves
+};
+
+// sums (nullable): finished by a warp that the product leaves idle.
 int launch_gemm(int64_t M, int64_t N, int64_t K, int type16, const GemmOperand &a,
-                const GemmOperand &b, const GemmEpilogue &epi, int32_t *dev_status,
-                cudaStream_t stream);
+                const GemmOperand &b, const GemmEpilogue &epi, GemmAfter after,
+                const ColumnSums *sums, int32_t *dev_status, cudaStream_t stream);
 
 // ---- activations ------------------------------------------------------------
 // 1 / (1 + exp(-x)) times n.  The intrinsics' errors (2 ulp of the quotient, a

@@ -75,7 +75,9 @@ struct GemmArgs {
     int a_mn, b_mn;     // operand has its own index contiguous
     int bn;             // columns per tile
     int n_tiles_m, n_tiles_n, n_tiles;
-    int stages, b_stage, b_box_rows;
+    int stages, b_stage;
+    int beside;         // BESIDE_GEMM
+    ColumnSums sums;    // part null: none
     uint32_t idesc;
     int bias_type, out_type, pre_type;
     int vec;            // 8 columns per access everywhere
@@ -384,6 +386,10 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
     if (CG == 2) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = sy.tmem_base;
+    // Nothing above touches the operands.  A product beside another one needs
+    // no wait here: that one has begun, so the passes before it are done.
+    if (!p.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int stage_bytes = A_STAGE + p.b_stage;
     auto epilogue = [&]() {
         // ================= epilogue =================
@@ -540,6 +546,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
         if (CG == 2 || SPLIT) cluster_sync();
         tc_fence_after();
         if (warp == 2) tmem_free<CG>(tmem);
+        // what follows on the stream must find the other product done too
+        if (p.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
         if (threadIdx.x == 0 && sy.abort_flag && p.dev_status) atomicOr(p.dev_status, SC_DEV_WAIT_LIMIT);
     };
     // 128 sums per epilogue thread: those warps take registers over from the
@@ -641,6 +649,17 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
                 int dummy = 0;
                 if (elect_one()) mma_commit<1>(&sy.drain);
                 mbar_wait(&sy.drain, 0, &dummy, WAIT_LIMIT_CYCLES / 16);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 3) {
+        // ================= column sums =================
+        if (p.sums.part) {
+            for (int64_t c = (int64_t)blockIdx.x * 32 + lane; c < p.sums.cols; c += (int64_t)gridDim.x * 32) {
+                float v = 0.f;
+#pragma unroll 16
+                for (int i = 0; i < p.sums.n; ++i) v += p.sums.part[i * p.sums.cols + c];
+                store_any(p.sums.out, p.sums.type, c, v);
             }
         }
         __syncwarp();

@@ -13,12 +13,21 @@ namespace {
 // workspace: 16-bit rows that do not start on 16-byte boundaries are copied
 // into rows that do, fp32 values are split into three bf16 planes, and the
 // backward pass turns dout into dz = dout act'(pre), summing its columns.
-struct PassArgs {
+struct PassJob {
     int64_t rows, cols, ld_in, ld_pre, ld_dst, plane;
     const void *in, *pre;  // pre: null without an activation
-    void *dst;
-    float *part;           // [gridDim.y][cols] column sums, or null
-    int act;
+    void *dst;             // null: column sums only
+    float *part;           // [chunks][cols] column sums, or null
+    int vec;               // 8 columns per access
+    int chunks;            // blocks that share the rows of one group of columns
+    int first_block;
+};
+// The passes of one call, run by one launch: job 0 may be dz (its own type and
+// activation), the others are copies.
+constexpr int MAX_JOBS = 3;
+struct PassArgs {
+    PassJob job[MAX_JOBS];
+    int n;
 };
 
 enum { OUT_NONE = 0, OUT_COPY = 1, OUT_PLANES = 3 };
@@ -34,107 +43,175 @@ __device__ __forceinline__ void split3(float x, __nv_bfloat16 (&p)[3]) {
     p[2] = __float2bfloat16_rn(r - __bfloat162float(p[1]));
 }
 
-// Bound by device memory.  A warp reads E columns per lane of one row at a
-// time; 8 warps of a block and gridDim.y blocks share the rows of 32 E columns.
-template <typename TIN, typename T, int E, int OUT, int ACT>
-__global__ void __launch_bounds__(256) pass_kernel(const PassArgs p) {
+// Columns of one block: 8 contiguous ones per lane, or (rows on no 16-byte
+// boundary) 4 per lane, 32 apart.
+constexpr int VEC_COLS = 256, SCALAR_COLS = 128;
+
+// One block's share of a job: 8 warps take a row each.  Bound by device memory.
+template <typename TIN, typename T, int OUT, int ACT, bool VEC>
+__device__ __forceinline__ void run_job(const PassJob &p, int block, float (*sums)[VEC_COLS]) {
+    constexpr int E = VEC ? 8 : 4, COLS = VEC ? VEC_COLS : SCALAR_COLS;
     const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
-    const int64_t col = ((int64_t)blockIdx.x * 32 + lane) * E;
+    const int64_t col0 = (int64_t)(block / p.chunks) * COLS;
+    const int chunk = block % p.chunks;
+    // column of the lane's element e
+    auto col = [&](int e) { return col0 + (VEC ? lane * 8 + e : lane + 32 * e); };
     float s[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) s[e] = 0.f;
-    if (col < p.cols) {
-        for (int64_t row = (int64_t)blockIdx.y * 8 + q; row < p.rows; row += (int64_t)gridDim.y * 8) {
-            float v[E];
-            load_vec<TIN, E>(static_cast<const TIN *>(p.in) + row * p.ld_in + col, v);
+    if (col(0) < p.cols) {
+        for (int64_t row = (int64_t)chunk * 8 + q; row < p.rows; row += (int64_t)p.chunks * 8) {
+            const TIN *in = static_cast<const TIN *>(p.in) + row * p.ld_in;
+            const T *pre = static_cast<const T *>(p.pre) + row * p.ld_pre;
+            float v[E], z[E];
+            if constexpr (VEC) {
+                load_vec<TIN, 8>(in + col(0), v);
+                if constexpr (ACT != SC_ACT_NONE) load_vec<T, 8>(pre + col(0), z);
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    v[e] = col(e) < p.cols ? to_f(in[col(e)]) : 0.f;
+                    if constexpr (ACT != SC_ACT_NONE) z[e] = col(e) < p.cols ? to_f(pre[col(e)]) : 0.f;
+                }
+            }
             if constexpr (ACT != SC_ACT_NONE) {
-                float z[E];
-                load_vec<T, E>(static_cast<const T *>(p.pre) + row * p.ld_pre + col, z);
 #pragma unroll
                 for (int e = 0; e < E; ++e) v[e] *= act_grad<ACT>(z[e]);
             }
 #pragma unroll
             for (int e = 0; e < E; ++e) s[e] += v[e];
             if constexpr (OUT == OUT_COPY) {
-                store_vec<T, E>(static_cast<T *>(p.dst) + row * p.ld_dst + col, v);
+                T *d = static_cast<T *>(p.dst) + row * p.ld_dst;
+                if constexpr (VEC) {
+                    store_vec<T, 8>(d + col(0), v);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        if (col(e) < p.cols) d[col(e)] = from_f<T>(v[e]);
+                }
             } else if constexpr (OUT == OUT_PLANES) {
-                __nv_bfloat16 *d = static_cast<__nv_bfloat16 *>(p.dst) + row * p.ld_dst + col;
-                alignas(16) __nv_bfloat16 o[3][E];
+                __nv_bfloat16 *d = static_cast<__nv_bfloat16 *>(p.dst) + row * p.ld_dst;
+                float o[3][E];
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
                     __nv_bfloat16 t[3];
                     split3(v[e], t);
 #pragma unroll
-                    for (int k = 0; k < 3; ++k) o[k][e] = t[k];
+                    for (int k = 0; k < 3; ++k) o[k][e] = __bfloat162float(t[k]);
                 }
 #pragma unroll
                 for (int k = 0; k < 3; ++k) {
-                    if constexpr (E == 8) *reinterpret_cast<uint4 *>(d + k * p.plane) = *reinterpret_cast<const uint4 *>(o[k]);
-                    else d[k * p.plane] = o[k][0];
+                    if constexpr (VEC) {
+                        store_vec<__nv_bfloat16, 8>(d + k * p.plane + col(0), o[k]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < E; ++e)
+                            if (col(e) < p.cols) d[k * p.plane + col(e)] = __float2bfloat16_rn(o[k][e]);
+                    }
                 }
             }
         }
     }
     if (!p.part) return;
-    __shared__ float sums[8][32 * E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) sums[q][lane * E + e] = s[e];
+    for (int e = 0; e < E; ++e) sums[q][col(e) - col0] = s[e];
     __syncthreads();
-    for (int i = threadIdx.x; i < 32 * E; i += 256) {
-        const int64_t c = (int64_t)blockIdx.x * 32 * E + i;
-        if (c >= p.cols) break;
-        float v = sums[0][i];
+    if (threadIdx.x < COLS && col0 + threadIdx.x < p.cols) {
+        float v = sums[0][threadIdx.x];
 #pragma unroll
-        for (int k = 1; k < 8; ++k) v += sums[k][i];
-        p.part[(int64_t)blockIdx.y * p.cols + c] = v;
+        for (int k = 1; k < 8; ++k) v += sums[k][threadIdx.x];
+        p.part[(int64_t)chunk * p.cols + col0 + threadIdx.x] = v;
     }
 }
 
-int pass_chunks(int64_t rows, int64_t cols) {
+template <typename TIN, typename T, int OUT0, int ACT>
+__global__ void __launch_bounds__(256) pass_kernel(const __grid_constant__ PassArgs p) {
+    // the matrix product that follows may set itself up now; it waits for this
+    // grid's end before it reads
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __shared__ float sums[8][VEC_COLS];
+    constexpr int OUT = sizeof(T) == 4 ? OUT_PLANES : OUT_COPY;
+    int j = 0;
+    while (j + 1 < p.n && (int)blockIdx.x >= p.job[j + 1].first_block) ++j;
+    const PassJob &job = p.job[j];
+    const int block = (int)blockIdx.x - job.first_block;
+    if (j == 0) {
+        if (job.vec) run_job<TIN, T, OUT0, ACT, true>(job, block, sums);
+        else run_job<TIN, T, OUT0, ACT, false>(job, block, sums);
+    } else {
+        if (job.vec) run_job<T, T, OUT, SC_ACT_NONE, true>(job, block, sums);
+        else run_job<T, T, OUT, SC_ACT_NONE, false>(job, block, sums);
+    }
+}
+
+// Partial rows of column sums: enough blocks to fill the device, few enough for
+// one warp to add them up while a matrix product runs.
+constexpr int MAX_CHUNKS = 64;
+
+int pass_chunks(int64_t rows, int64_t cols, bool vec) {
     if (rows < 1 || cols < 1) return 1;
-    int64_t c = div_up(8 * (int64_t)sm_count(), div_up(cols, 256));
+    int64_t c = div_up(8 * (int64_t)sm_count(), div_up(cols, vec ? VEC_COLS : SCALAR_COLS));
     if (c > div_up(rows, 8)) c = div_up(rows, 8);
-    return (int)c;
+    return (int)(c < MAX_CHUNKS ? c : MAX_CHUNKS);
 }
 
-template <typename TIN, typename T, int OUT, int ACT>
-void pass(const PassArgs &p, bool vec, int chunks, cudaStream_t s) {
-    if (vec) pass_kernel<TIN, T, 8, OUT, ACT><<<dim3((unsigned)div_up(p.cols, 256), (unsigned)chunks), 256, 0, s>>>(p);
-    else pass_kernel<TIN, T, 1, OUT, ACT><<<dim3((unsigned)div_up(p.cols, 32), (unsigned)chunks), 256, 0, s>>>(p);
-}
-
-template <typename TIN, typename T, int OUT>
-void pass_act(const PassArgs &p, bool vec, int chunks, cudaStream_t s) {
-    switch (p.pre ? p.act : SC_ACT_NONE) {
-        case SC_ACT_RELU: return pass<TIN, T, OUT, SC_ACT_RELU>(p, vec, chunks, s);
-        case SC_ACT_GELU: return pass<TIN, T, OUT, SC_ACT_GELU>(p, vec, chunks, s);
-        case SC_ACT_GELU_TANH: return pass<TIN, T, OUT, SC_ACT_GELU_TANH>(p, vec, chunks, s);
-        case SC_ACT_SILU: return pass<TIN, T, OUT, SC_ACT_SILU>(p, vec, chunks, s);
-        default: return pass<TIN, T, OUT, SC_ACT_NONE>(p, vec, chunks, s);
+template <typename TIN, typename T, int OUT0>
+int launch_pass_act(const PassArgs &p, int act, int blocks, cudaStream_t s) {
+    switch (act) {
+        case SC_ACT_RELU: pass_kernel<TIN, T, OUT0, SC_ACT_RELU><<<blocks, 256, 0, s>>>(p); break;
+        case SC_ACT_GELU: pass_kernel<TIN, T, OUT0, SC_ACT_GELU><<<blocks, 256, 0, s>>>(p); break;
+        case SC_ACT_GELU_TANH: pass_kernel<TIN, T, OUT0, SC_ACT_GELU_TANH><<<blocks, 256, 0, s>>>(p); break;
+        case SC_ACT_SILU: pass_kernel<TIN, T, OUT0, SC_ACT_SILU><<<blocks, 256, 0, s>>>(p); break;
+        default: pass_kernel<TIN, T, OUT0, SC_ACT_NONE><<<blocks, 256, 0, s>>>(p); break;
     }
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? SC_OK : cuda_fail(e, "sc_linear: operand pass");
 }
-
 template <typename TIN, typename T, int OUT>
-void pass_out(const PassArgs &p, bool vec, int chunks, cudaStream_t s) {
-    if (p.dst) pass_act<TIN, T, OUT>(p, vec, chunks, s);
-    else pass_act<TIN, T, OUT_NONE>(p, vec, chunks, s);
+int launch_pass_out(const PassArgs &p, int act, int blocks, cudaStream_t s) {
+    return p.job[0].dst ? launch_pass_act<TIN, T, OUT>(p, act, blocks, s)
+                        : launch_pass_act<TIN, T, OUT_NONE>(p, act, blocks, s);
 }
 
 bool rows_ok(const void *p, int64_t ld, int type) { return aligned16(p) && ld * type_size(type) % 16 == 0; }
 
-// One pass; `type` is the operand type, `in_type` what is read.
-int launch_pass(const PassArgs &p, int in_type, int type, cudaStream_t s) {
-    const bool vec = p.cols % 8 == 0 && rows_ok(p.in, p.ld_in, in_type) && (!p.pre || rows_ok(p.pre, p.ld_pre, type));
-    const int chunks = pass_chunks(p.rows, p.cols);
-    using bf = __nv_bfloat16;
-    if (type == SC_F32) pass_out<float, float, OUT_PLANES>(p, vec, chunks, s);
-    else if (type == SC_BF16 && in_type == SC_F32) pass_out<float, bf, OUT_COPY>(p, vec, chunks, s);
-    else if (type == SC_BF16) pass_out<bf, bf, OUT_COPY>(p, vec, chunks, s);
-    else if (in_type == SC_F32) pass_out<float, __half, OUT_COPY>(p, vec, chunks, s);
-    else pass_out<__half, __half, OUT_COPY>(p, vec, chunks, s);
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? SC_OK : cuda_fail(e, "sc_linear: operand pass");
-}
+// The passes of a call; `type` is the operand type.
+struct Passes {
+    PassArgs a = {};
+    int act0 = SC_ACT_NONE, in0 = SC_F32;  // of job 0
+
+    void add(const PassJob &j, int in_type, int act, int type) {
+        if (a.n == 0) {
+            act0 = act;
+            in0 = in_type;
+        }
+        PassJob &o = a.job[a.n++];
+        o = j;
+        o.vec = j.cols % 8 == 0 && rows_ok(j.in, j.ld_in, in_type) && (!j.pre || rows_ok(j.pre, j.ld_pre, type));
+    }
+    int launch(int type, cudaStream_t s) {
+        if (a.n == 0) return SC_OK;
+        int64_t blocks = 0;
+        for (int i = 0; i < a.n; ++i) {
+            PassJob &j = a.job[i];
+            if (blocks > INT32_MAX / 2) break;
+            j.chunks = pass_chunks(j.rows, j.cols, j.vec);
+            j.first_block = (int)blocks;
+            blocks += div_up(j.cols, j.vec ? VEC_COLS : SCALAR_COLS) * j.chunks;
+        }
+        if (blocks > INT32_MAX / 2) {
+            set_error("sc_linear: the operands are too large");
+            return SC_ERR_ARG;
+        }
+        using bf = __nv_bfloat16;
+        const int n = (int)blocks;
+        if (type == SC_F32) return launch_pass_out<float, float, OUT_PLANES>(a, act0, n, s);
+        if (type == SC_BF16 && in0 == SC_F32) return launch_pass_out<float, bf, OUT_COPY>(a, act0, n, s);
+        if (type == SC_BF16) return launch_pass_out<bf, bf, OUT_COPY>(a, act0, n, s);
+        if (in0 == SC_F32) return launch_pass_out<float, __half, OUT_COPY>(a, act0, n, s);
+        return launch_pass_out<__half, __half, OUT_COPY>(a, act0, n, s);
+    }
+};
 
 // ---- operands ---------------------------------------------------------------
 int tc_type(int type) { return type == SC_F32 ? SC_BF16 : type; }
@@ -163,24 +240,27 @@ GemmOperand copied(void *p, int64_t rows, int64_t cols, int type) {
 }
 
 // The operand as the matrix product reads it: in place, or through a pass.
-int operand(const void *p, int64_t rows, int64_t cols, int64_t ld, int type, Scratch &ws, GemmOperand &o, cudaStream_t s) {
+GemmOperand operand(const void *p, int64_t rows, int64_t cols, int64_t ld, int type, bool k_major, Scratch &ws,
+                    Passes &passes) {
+    GemmOperand o = {};
     if (in_place(p, ld, type)) {
-        o = {};
         o.p = p;
         o.ld = ld;
         o.planes = 1;
-        return SC_OK;
+    } else {
+        o = copied(ws.take(copy_bytes(rows, cols, type)), rows, cols, type);
+        PassJob j = {};
+        j.rows = rows;
+        j.cols = cols;
+        j.ld_in = ld;
+        j.in = p;
+        j.dst = const_cast<void *>(o.p);
+        j.ld_dst = o.ld;
+        j.plane = o.plane_stride;
+        passes.add(j, type, SC_ACT_NONE, type);
     }
-    o = copied(ws.take(copy_bytes(rows, cols, type)), rows, cols, type);
-    PassArgs a = {};
-    a.rows = rows;
-    a.cols = cols;
-    a.ld_in = ld;
-    a.in = p;
-    a.dst = const_cast<void *>(o.p);
-    a.ld_dst = o.ld;
-    a.plane = o.plane_stride;
-    return launch_pass(a, type, type, s);
+    o.k_major = k_major;
+    return o;
 }
 
 // ---- checks and workspace ---------------------------------------------------
@@ -237,7 +317,7 @@ bool dz_in_place(const sc_linear_desc &d, const void *dout) {
 }
 
 int64_t part_bytes(const sc_linear_desc &d) {
-    return round_up((int64_t)pass_chunks(d.M, d.N) * d.N * (int64_t)sizeof(float), 256);
+    return round_up(MAX_CHUNKS * d.N * (int64_t)sizeof(float), 256);
 }
 
 int64_t bwd_workspace(const sc_linear_desc &d, const void *dout, const void *x, const void *w) {
@@ -285,10 +365,10 @@ extern "C" int sc_linear(const sc_linear_desc *d, const void *x, const void *w, 
     if (int rc = check_workspace(*d, fwd_workspace(*d, x, w), who)) return rc;
     const cudaStream_t s = (cudaStream_t)stream;
     Scratch ws = {static_cast<char *>(d->workspace)};
-    GemmOperand a, b;
-    if (int rc = operand(x, d->M, d->K, d->ld_x, d->type, ws, a, s)) return rc;
-    if (int rc = operand(w, d->N, d->K, d->ld_w, d->type, ws, b, s)) return rc;
-    a.k_major = b.k_major = true;
+    Passes passes;
+    const GemmOperand a = operand(x, d->M, d->K, d->ld_x, d->type, true, ws, passes);
+    const GemmOperand b = operand(w, d->N, d->K, d->ld_w, d->type, true, ws, passes);
+    if (int rc = passes.launch(d->type, s)) return rc;
     GemmEpilogue e = {};
     e.bias = bias;
     e.res = residual;
@@ -301,7 +381,7 @@ extern "C" int sc_linear(const sc_linear_desc *d, const void *x, const void *w, 
     e.out_type = d->out_type;
     e.pre_type = d->type;
     e.act = d->act;
-    return launch_gemm(d->M, d->N, d->K, tc_type(d->type), a, b, e, dev_status, s);
+    return launch_gemm(d->M, d->N, d->K, tc_type(d->type), a, b, e, passes.a.n ? AFTER_PASS : AFTER_ANY, nullptr, dev_status, s);
 }
 
 extern "C" int sc_linear_backward(const sc_linear_desc *d, const void *dout, const void *x,
@@ -339,17 +419,18 @@ extern "C" int sc_linear_backward(const sc_linear_desc *d, const void *dout, con
         return e == cudaSuccess ? SC_OK : cuda_fail(e, who);
     }
     Scratch ws = {static_cast<char *>(d->workspace)};
-    GemmOperand dz = {};
-    PassArgs p = {};
+    Passes passes;
+    ColumnSums sums = {};
+    PassJob p = {};
     p.rows = d->M;
     p.cols = d->N;
     p.ld_in = d->ld_out;
     p.ld_pre = d->ld_pre;
     p.in = dout;
     p.pre = pre;
-    p.act = d->act;
     float *part = static_cast<float *>(ws.take(part_bytes(*d)));
     p.part = dbias ? part : nullptr;
+    GemmOperand dz = {};
     if (dz_in_place(*d, dout)) {
         dz.p = dout;
         dz.ld = d->ld_out;
@@ -360,28 +441,39 @@ extern "C" int sc_linear_backward(const sc_linear_desc *d, const void *dout, con
         p.ld_dst = dz.ld;
         p.plane = dz.plane_stride;
     }
-    if (p.dst || p.part)
-        if (int rc = launch_pass(p, d->out_type, d->type, s)) return rc;
+    if (p.dst || p.part) passes.add(p, d->out_type, d->act, d->type);
+    GemmOperand bw = {}, bx = {};
+    if (dx) bw = operand(w, d->N, d->K, d->ld_w, d->type, false, ws, passes);
+    if (dw) bx = operand(x, d->M, d->K, d->ld_x, d->type, false, ws, passes);
+    if (int rc = passes.launch(d->type, s)) return rc;
+    if (dbias) {
+        sums.part = part;
+        sums.n = passes.a.job[0].chunks;
+        sums.cols = d->N;
+        sums.out = dbias;
+        sums.type = d->grad_type;
+    }
     GemmEpilogue e = {};
-    GemmOperand b;
     if (dx) {
-        if (int rc = operand(w, d->N, d->K, d->ld_w, d->type, ws, b, s)) return rc;
         dz.k_major = true;
-        b.k_major = false;
         e.out = dx;
         e.ld_out = d->ld_dx;
         e.out_type = d->type;
-        if (int rc = launch_gemm(d->M, d->K, d->N, tc_type(d->type), dz, b, e, dev_status, s)) return rc;
+        if (int rc = launch_gemm(d->M, d->K, d->N, tc_type(d->type), dz, bw, e, passes.a.n ? AFTER_PASS : AFTER_ANY,
+                                 dbias && !dw ? &sums : nullptr, dev_status, s))
+            return rc;
     }
     if (dw) {
-        if (int rc = operand(x, d->M, d->K, d->ld_x, d->type, ws, b, s)) return rc;
         dz.k_major = false;
-        b.k_major = false;
         e.out = dw;
         e.ld_out = d->ld_dw;
         e.out_type = d->grad_type;
-        if (int rc = launch_gemm(d->N, d->K, d->M, tc_type(d->type), dz, b, e, dev_status, s)) return rc;
+        if (int rc = launch_gemm(d->N, d->K, d->M, tc_type(d->type), dz, bx, e,
+                                 dx ? BESIDE_GEMM : passes.a.n ? AFTER_PASS : AFTER_ANY, dbias ? &sums : nullptr,
+                                 dev_status, s))
+            return rc;
     }
-    if (dbias) return launch_finish_columns(part, pass_chunks(d->M, d->N), 1, d->N, dbias, nullptr, d->grad_type, s);
+    if (dbias && !dx && !dw)
+        return launch_finish_columns(sums.part, sums.n, 1, sums.cols, dbias, nullptr, sums.type, s);
     return SC_OK;
 }
