@@ -56,15 +56,15 @@ __device__ __forceinline__ void unpack2<__half>(uint32_t w, float &a, float &b) 
 }
 
 // E contiguous elements to and from fp32 registers.  E * sizeof(T) is 16 or 32
-// bytes on a 16-byte boundary, 8 bytes on an 8-byte boundary, or one element.
+// bytes on a 16-byte boundary, 8 or 4 bytes on such a boundary, or one element.
 template <typename T, int E>
 __device__ __forceinline__ void load_vec(const T *p, float (&v)[E]) {
     constexpr int B = E * (int)sizeof(T);
     if constexpr (E == 1) {
         v[0] = to_f(*p);
     } else {
-        static_assert(B == 8 || B % 16 == 0, "vector width");
-        constexpr int W = B == 8 ? 2 : 4;  // 32-bit words per load
+        static_assert(B == 4 || B == 8 || B % 16 == 0, "vector width");
+        constexpr int W = B < 16 ? B / 4 : 4;  // 32-bit words per load
         uint32_t raw[B / 4];
 #pragma unroll
         for (int i = 0; i < B / 4 / W; ++i) {
@@ -74,10 +74,12 @@ __device__ __forceinline__ void load_vec(const T *p, float (&v)[E]) {
                 raw[4 * i + 1] = q.y;
                 raw[4 * i + 2] = q.z;
                 raw[4 * i + 3] = q.w;
-            } else {
+            } else if constexpr (W == 2) {
                 const uint2 q = reinterpret_cast<const uint2 *>(p)[i];
                 raw[2 * i] = q.x;
                 raw[2 * i + 1] = q.y;
+            } else {
+                raw[i] = reinterpret_cast<const uint32_t *>(p)[i];
             }
         }
         if constexpr (sizeof(T) == 4) {
@@ -96,8 +98,8 @@ __device__ __forceinline__ void store_vec(T *p, const float (&v)[E]) {
     if constexpr (E == 1) {
         *p = from_f<T>(v[0]);
     } else {
-        static_assert(B == 8 || B % 16 == 0, "vector width");
-        constexpr int W = B == 8 ? 2 : 4;
+        static_assert(B == 4 || B == 8 || B % 16 == 0, "vector width");
+        constexpr int W = B < 16 ? B / 4 : 4;
         uint32_t e[B / 4];
         if constexpr (sizeof(T) == 4) {
 #pragma unroll
@@ -110,8 +112,10 @@ __device__ __forceinline__ void store_vec(T *p, const float (&v)[E]) {
         for (int i = 0; i < B / 4 / W; ++i) {
             if constexpr (W == 4)
                 reinterpret_cast<uint4 *>(p)[i] = make_uint4(e[4 * i], e[4 * i + 1], e[4 * i + 2], e[4 * i + 3]);
-            else
+            else if constexpr (W == 2)
                 reinterpret_cast<uint2 *>(p)[i] = make_uint2(e[2 * i], e[2 * i + 1]);
+            else
+                reinterpret_cast<uint32_t *>(p)[i] = e[i];
         }
     }
 }

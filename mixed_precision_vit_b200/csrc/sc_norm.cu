@@ -6,14 +6,17 @@
 //   dx = r (g - (s1 + h s2) / D) [+ dx_add],
 //   dw_j = sum_i dy_ij h_ij,  db_j = sum_i dy_ij.
 // Both are bound by device memory: a row is read once and held in registers.
+#include <initializer_list>
+#include <type_traits>
+
 #include "sc_layers.cuh"
 
 namespace scb {
 namespace {
 
-// Blocks per SM that hold column sums in the backward pass: one partial row of
-// dweight and dbias each.
-constexpr int BWD_BLOCKS_PER_SM = 3;
+// Most blocks (one per SM) that hold column sums in the backward pass, a
+// partial row of dweight and dbias each; even, see Pairs.
+int bwd_blocks() { return sm_count() + (sm_count() & 1); }
 
 struct NormArgs {
     int64_t rows, cols;
@@ -145,54 +148,231 @@ __global__ void __launch_bounds__(512) ln_fwd_wide_kernel(const NormArgs p) {
     }
 }
 
-// Backward with the row in registers: T threads per row as in the forward,
-// NT / T rows per block at a time; every thread sums dy h and dy over the
-// block's rows for its own columns, and the block writes one partial row of
-// each (summed over blocks by finish_columns_kernel).
+// ---- rows in registers, any alignment ----------------------------------------
+// A group of T threads walks rows, chunk c of thread t covering E columns from
+// (c T + t) E - shift on.  With E = 8 or 4 rows are aligned and the shift is 0.
+// Rows of an odd stride start on every other 2-element boundary only: with E =
+// 2 ("Pairs") the shift is the parity of row * ld, so that every access of two
+// elements is aligned; the groups' number is even, so a group's rows all have
+// the same shift and its columns stay the same.  Elements outside the row (the
+// shifted first pair, a last half pair) are left out.
+template <typename T, int E>
+__device__ __forceinline__ void load_cols(const T *row, int col, int D, float (&v)[E], float fill) {
+    if (col >= 0 && col + E <= D) {
+        load_vec<T, E>(row + col, v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = col + e >= 0 && col + e < D ? to_f(row[col + e]) : fill;
+    }
+}
+template <typename T, int E>
+__device__ __forceinline__ void store_cols(T *row, int col, int D, const float (&v)[E]) {
+    if (col >= 0 && col + E <= D) {
+        store_vec<T, E>(row + col, v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (col + e >= 0 && col + e < D) row[col + e] = from_f<T>(v[e]);
+    }
+}
+// E elements as they lie in memory, so that values loaded ahead take no more
+// registers than bytes.
+template <typename T, int E>
+struct Raw {
+    static constexpr int N = (E * (int)sizeof(T) + 3) / 4;
+    uint32_t w[N];
+    __device__ __forceinline__ void load(const T *row, int col, int D) {
+        constexpr int B = E * (int)sizeof(T);
+        if (B >= 4 && col >= 0 && col + E <= D) {
+            if constexpr (B >= 16) {
+#pragma unroll
+                for (int i = 0; i < B / 16; ++i) {
+                    const uint4 q = reinterpret_cast<const uint4 *>(row + col)[i];
+                    w[4 * i] = q.x;
+                    w[4 * i + 1] = q.y;
+                    w[4 * i + 2] = q.z;
+                    w[4 * i + 3] = q.w;
+                }
+            } else if constexpr (B == 8) {
+                const uint2 q = *reinterpret_cast<const uint2 *>(row + col);
+                w[0] = q.x;
+                w[1] = q.y;
+            } else if constexpr (B == 4) {
+                w[0] = *reinterpret_cast<const uint32_t *>(row + col);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) w[i] = 0;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                if (col + e < 0 || col + e >= D) continue;
+                if constexpr (sizeof(T) == 4) w[e] = __float_as_uint(row[col + e]);
+                else w[e / 2] |= (uint32_t) * reinterpret_cast<const uint16_t *>(row + col + e) << (16 * (e & 1));
+            }
+        }
+    }
+    __device__ __forceinline__ void get(float (&v)[E]) const {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[e] = __uint_as_float(w[e]);
+        } else if constexpr (E == 1) {
+            float b;
+            unpack2<T>(w[0], v[0], b);
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; e += 2) unpack2<T>(w[e / 2], v[e], v[e + 1]);
+        }
+    }
+};
+__device__ __forceinline__ float param(const void *p, int type, int col, int D, float otherwise) {
+    float v[1] = {otherwise};
+    if (p && col >= 0 && col < D) load_any<1>(p, type, col, v);
+    return v[0];
+}
+
+// Sums of two values over the T threads of group g; `red` holds two floats per
+// warp of the block, consecutive calls use different ones.
+template <int T, int NT>
+__device__ __forceinline__ void group_sum2(float &a, float &b, float (*red)[2], int g) {
+    a = warp_sum(a);
+    b = warp_sum(b);
+    if constexpr (T > 32) {
+        const int w = threadIdx.x >> 5, w0 = g * (T / 32);
+        if ((threadIdx.x & 31) == 0) {
+            red[w][0] = a;
+            red[w][1] = b;
+        }
+        if constexpr (T == NT) __syncthreads();
+        else asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "n"(T) : "memory");
+        a = red[w0][0];
+        b = red[w0][1];
+#pragma unroll
+        for (int i = 1; i < T / 32; ++i) {
+            a += red[w0 + i][0];
+            b += red[w0 + i][1];
+        }
+    }
+}
+
+// Forward of rows that no 16-byte access fits: weight and bias stay in
+// registers over a group's rows.  4099 x 997 bf16 -> fp32: see the table of
+// measurements; one element per access took 17 us.
 template <typename TX, typename TY, int E, int NC, int T, int NT>
-__global__ void __launch_bounds__(NT) ln_bwd_kernel(const NormArgs p) {
-    static_assert(T == 32 || T == NT, "a warp or the block per row");
+__global__ void __launch_bounds__(NT) ln_fwd_any_kernel(const NormArgs p) {
     constexpr int G = NT / T;
-    extern __shared__ float slices[];  // T = 32: [G / 2][2][cols] when the column sums are wanted
-    __shared__ float red[2][2][T / 32];
-    const int t = threadIdx.x % T, g = threadIdx.x / T;
+    __shared__ float red[2][NT / 32][2];
+    const int t = threadIdx.x % T, g = threadIdx.x / T, D = (int)p.cols;
+    const int64_t first = (int64_t)blockIdx.x * G + g, step = (int64_t)gridDim.x * G;
+    const int shift = E == 2 ? (int)((first * p.ld_x) & 1) : 0;
+    float w[NC][E], b[NC][E];
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int col = (c * T + t) * E - shift + e;
+            w[c][e] = param(p.w, p.w_type, col, D, 1.f);
+            b[c][e] = param(p.b, p.w_type, col, D, 0.f);
+        }
+    const float inv = 1.f / (float)D;
+    for (int64_t row = first; row < p.rows; row += step) {
+        const TX *x = static_cast<const TX *>(p.x) + row * p.ld_x;
+        float v[NC][E];
+        float s = 0.f, unused = 0.f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) load_cols<TX, E>(x, (c * T + t) * E - shift, D, v[c], 0.f);
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int e = 0; e < E; ++e) s += v[c][e];
+        group_sum2<T, NT>(s, unused, red[0], g);
+        const float mu = s * inv;
+        s = 0.f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int col = (c * T + t) * E - shift + e;
+                const float d = v[c][e] - mu;
+                if (col >= 0 && col < D) s += d * d;
+            }
+        group_sum2<T, NT>(s, unused, red[1], g);
+        const float r = 1.f / sqrtf(s * inv + p.eps);
+        if (t == 0) {
+            if (p.mean) p.mean[row] = mu;
+            if (p.rstd) p.rstd[row] = r;
+        }
+        TY *y = static_cast<TY *>(p.y) + row * p.ld_y;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) v[c][e] = (v[c][e] - mu) * r * w[c][e] + b[c][e];
+            store_cols<TY, E>(y, (c * T + t) * E - shift, D, v[c]);
+        }
+    }
+}
+
+// Backward: every thread sums dy h and dy over its group's rows for its own
+// columns; the block adds its groups' sums up in shared memory and writes one
+// partial row of each (summed over blocks by finish_columns_kernel).  One block
+// of 512 threads per SM keeps the partial rows few; its groups' rows in flight
+// hide the memory's latency.
+template <typename TX, typename TY, int E, int NC, int T, int NT>
+__global__ void __launch_bounds__(NT, 1) ln_bwd_kernel(const NormArgs p) {
+    constexpr int G = NT / T;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // [cols + 2] weights at 1 (a shifted first column is -1); then, for the
+    // column sums, [G / 2][2][T * NC * E]
+    extern __shared__ __align__(16) float smem[];
+    __shared__ float red[2][NT / 32][2];
+    const int t = threadIdx.x % T, g = threadIdx.x / T, D = (int)p.cols;
+    const int64_t first = (int64_t)blockIdx.x * G + g, step = (int64_t)gridDim.x * G;
+    const int shift = E == 2 ? (int)((first * p.ld_x) & 1) : 0;
+    float *weight = smem + 4;  // keeps column 0 on a 16-byte boundary
+    for (int i = (int)threadIdx.x - 1; i < T * NC * E; i += NT) weight[i] = param(p.w, p.w_type, i, D, 1.f);
+    __syncthreads();
     float dw[NC][E], db[NC][E];
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
         for (int e = 0; e < E; ++e) dw[c][e] = db[c][e] = 0.f;
-    const float inv = 1.f / (float)p.cols;
+    const float inv = 1.f / (float)D;
     int par = 0;
-    for (int64_t row = (int64_t)blockIdx.x * G + g; row < p.rows; row += (int64_t)gridDim.x * G) {
+    // the next row's values, loaded while the current one is worked on
+    Raw<TX, E> nx[NC];
+    Raw<TY, E> nd[NC];
+    float nmu = 0.f, nr = 0.f;
+    auto fetch = [&](int64_t row) {
+        if (row >= p.rows) return;
         const TX *x = static_cast<const TX *>(p.x) + row * p.ld_x;
         const TY *dy = static_cast<const TY *>(p.dy) + row * p.ld_y;
-        const float mu = p.mean[row], r = p.rstd[row];
-        float h[NC][E], d[NC][E];
+        nmu = p.mean[row];
+        nr = p.rstd[row];
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            const int64_t col = (int64_t)(c * T + t) * E;
-            if (col < p.cols) {
-                load_vec<TX, E>(x + col, h[c]);
-                load_vec<TY, E>(dy + col, d[c]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    h[c][e] = mu;
-                    d[c][e] = 0.f;
-                }
-            }
+            nx[c].load(x, (c * T + t) * E - shift, D);
+            nd[c].load(dy, (c * T + t) * E - shift, D);
         }
+    };
+    fetch(first);
+    for (int64_t row = first; row < p.rows; row += step) {
+        const float mu = nmu, r = nr;
+        float h[NC][E], d[NC][E];
         float s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            const int64_t col = (int64_t)(c * T + t) * E;
-            if (col >= p.cols) continue;
+            const int col = (c * T + t) * E - shift;
             float w[E];
+            if constexpr (E >= 4) {
+                load_vec<float, E>(weight + col, w);
+            } else {
 #pragma unroll
-            for (int e = 0; e < E; ++e) w[e] = 1.f;
-            if (p.w) load_any<E>(p.w, p.w_type, col, w);
+                for (int e = 0; e < E; ++e) w[e] = weight[col + e];
+            }
+            nx[c].get(h[c]);
+            nd[c].get(d[c]);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
+                // dy is 0 outside the row, so nothing there counts
                 h[c][e] = (h[c][e] - mu) * r;
                 dw[c][e] += d[c][e] * h[c][e];
                 db[c][e] += d[c][e];
@@ -201,88 +381,74 @@ __global__ void __launch_bounds__(NT) ln_bwd_kernel(const NormArgs p) {
                 s2 += d[c][e] * h[c][e];
             }
         }
+        fetch(row + step);
         if (!p.y) continue;
-        if constexpr (T == 32) {
-            s1 = warp_sum(s1);
-            s2 = warp_sum(s2);
-        } else {
-            s1 = warp_sum(s1);
-            s2 = warp_sum(s2);
-            if ((threadIdx.x & 31) == 0) {
-                red[par][0][threadIdx.x >> 5] = s1;
-                red[par][1][threadIdx.x >> 5] = s2;
-            }
-            __syncthreads();
-            s1 = red[par][0][0];
-            s2 = red[par][1][0];
-#pragma unroll
-            for (int i = 1; i < T / 32; ++i) {
-                s1 += red[par][0][i];
-                s2 += red[par][1][i];
-            }
-            par ^= 1;
-        }
+        group_sum2<T, NT>(s1, s2, red[par], g);
+        par ^= 1;
         s1 *= inv;
         s2 *= inv;
         TX *dx = static_cast<TX *>(p.y) + row * p.ld_dx;
         const TX *add = static_cast<const TX *>(p.add) + row * p.ld_add;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            const int64_t col = (int64_t)(c * T + t) * E;
-            if (col >= p.cols) continue;
+            const int col = (c * T + t) * E - shift;
             float a[E];
 #pragma unroll
             for (int e = 0; e < E; ++e) a[e] = 0.f;
-            if (p.add) load_vec<TX, E>(add + col, a);
+            if (p.add) load_cols<TX, E>(add, col, D, a, 0.f);
 #pragma unroll
             for (int e = 0; e < E; ++e) a[e] += r * (d[c][e] - (s1 + h[c][e] * s2));
-            store_vec<TX, E>(dx + col, a);
+            store_cols<TX, E>(dx, col, D, a);
         }
     }
     if (!p.part) return;
-    float *out = p.part + (int64_t)blockIdx.x * 2 * p.cols;
-    if constexpr (G > 1) {
-        // halve the warps until one holds the block's sums
+    // Columns by number, so that groups of either shift add up.  Each column
+    // belongs to one thread of a group, and a barrier separates the steps.
+    constexpr int W = T * NC * E;
+    float *slices = smem + 4 + W + 4;
 #pragma unroll
-        for (int half = G / 2; half >= 1; half /= 2) {
-            if (g >= half && g < 2 * half) {
-                float *s = slices + (int64_t)(g - half) * 2 * p.cols;
+    for (int half = G / 2; half >= 1; half /= 2) {
+        if (g >= half && g < 2 * half) {
+            float *s = slices + (g - half) * 2 * W;
 #pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    const int64_t col = (int64_t)(c * T + t) * E;
-                    if (col >= p.cols) continue;
-                    store_vec<float, E>(s + col, dw[c]);
-                    store_vec<float, E>(s + p.cols + col, db[c]);
-                }
-            }
-            __syncthreads();
-            if (g < half) {
-                const float *s = slices + (int64_t)g * 2 * p.cols;
+            for (int c = 0; c < NC; ++c)
 #pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    const int64_t col = (int64_t)(c * T + t) * E;
-                    if (col >= p.cols) continue;
-                    float a[E], b[E];
-                    load_vec<float, E>(s + col, a);
-                    load_vec<float, E>(s + p.cols + col, b);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        dw[c][e] += a[e];
-                        db[c][e] += b[e];
+                for (int e = 0; e < E; ++e) {
+                    const int col = (c * T + t) * E - shift + e;
+                    if (col >= 0 && col < D) {
+                        s[col] = dw[c][e];
+                        s[W + col] = db[c][e];
                     }
                 }
-            }
-            __syncthreads();
         }
-        if (g != 0) return;
-    }
+        __syncthreads();
+        if (g < half) {
+            const float *s = slices + g * 2 * W;
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-        const int64_t col = (int64_t)(c * T + t) * E;
-        if (col >= p.cols) continue;
-        store_vec<float, E>(out + col, dw[c]);
-        store_vec<float, E>(out + p.cols + col, db[c]);
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const int col = (c * T + t) * E - shift + e;
+                    if (col >= 0 && col < D) {
+                        dw[c][e] += s[col];
+                        db[c][e] += s[W + col];
+                    }
+                }
+        }
+        __syncthreads();
     }
+    if (g != 0) return;
+    float *out = p.part + (int64_t)blockIdx.x * 2 * D;
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int col = (c * T + t) * E - shift + e;
+            if (col >= 0 && col < D) {
+                out[col] = dw[c][e];
+                out[D + col] = db[c][e];
+            }
+        }
 }
 
 // Backward of rows too wide for registers: dx by one block per row in two
@@ -362,6 +528,7 @@ __global__ void __launch_bounds__(256) ln_bwd_wide_cols_kernel(const NormArgs p)
 __global__ void __launch_bounds__(512) finish_columns_kernel(const float *part, int n_part, int n_out,
                                                              int64_t cols, void *out0, void *out1,
                                                              int out_type) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     __shared__ float s[16][33];
     const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
     const int64_t i = (int64_t)blockIdx.x * 32 + lane, n = (int64_t)n_out * cols;
@@ -386,66 +553,98 @@ void fwd(const NormArgs &a, cudaStream_t s) {
     ln_fwd_kernel<TX, TY, E, NC, T><<<(unsigned)div_up(a.rows, NT / T), NT, 0, s>>>(a);
 }
 
-template <typename TX, typename TY, bool VEC>
-void fwd_rows(const NormArgs &a, cudaStream_t s) {
-    // 8 columns per access (16 bytes of a 16-bit type), 4 where both are fp32;
-    // one where rows are not aligned.  At most 32 values per thread.
-    constexpr int E = !VEC ? 1 : (sizeof(TX) == 4 && sizeof(TY) == 4 ? 4 : 8);
-    const int64_t D = a.cols;
-    if (D <= 256) fwd<TX, TY, E, 8 / E, 32>(a, s);
-    else if (D <= 512) fwd<TX, TY, E, 16 / E, 32>(a, s);
-    else if (D <= 1024) fwd<TX, TY, E, 32 / E, 32>(a, s);
-    else if (D <= 4096) fwd<TX, TY, E, 32 / E, 128>(a, s);
-    else if (D <= 16384) fwd<TX, TY, E, 32 / E, 512>(a, s);
-    else ln_fwd_wide_kernel<TX, TY, E><<<(unsigned)a.rows, 512, 0, s>>>(a);
+template <typename TX, typename TY, int E, int T, int NT>
+void fwd_any(const NormArgs &a, cudaStream_t s) {
+    const int64_t most = 4 * sm_count();
+    int64_t blocks = div_up(a.rows, NT / T) < most ? div_up(a.rows, NT / T) : most;
+    blocks += blocks & 1;
+    ln_fwd_any_kernel<TX, TY, E, 16 / E, T, NT><<<(unsigned)blocks, NT, 0, s>>>(a);
 }
 
-template <typename TX, typename TY, int E, int NC, int T, int NT>
-int bwd(const NormArgs &a, int blocks, cudaStream_t s) {
-    const size_t smem = a.part && T < NT ? (size_t)(NT / T / 2) * 2 * a.cols * sizeof(float) : 0;
-    ln_bwd_kernel<TX, TY, E, NC, T, NT><<<(unsigned)blocks, NT, smem, s>>>(a);
-    return blocks;
+// How the rows lie: 16-byte accesses of every row, 2-element accesses (Pairs),
+// or neither.
+enum Access { VEC, PAIRS, SINGLE };
+
+template <typename TX, typename TY, int ACCESS>
+void fwd_rows(const NormArgs &a, cudaStream_t s) {
+    // VEC: 8 columns per access (16 bytes of a 16-bit type), 4 where both are
+    // fp32, and at most 32 values per thread; otherwise 16 values.
+    const int64_t D = a.cols;
+    constexpr int E = ACCESS == SINGLE ? 1 : ACCESS == PAIRS ? 2 : sizeof(TX) == 4 && sizeof(TY) == 4 ? 4 : 8;
+    if constexpr (ACCESS == VEC) {
+        if (D <= 256) return fwd<TX, TY, E, 8 / E, 32>(a, s);
+        if (D <= 512) return fwd<TX, TY, E, 16 / E, 32>(a, s);
+        if (D <= 1024) return fwd<TX, TY, E, 32 / E, 32>(a, s);
+        if (D <= 4096) return fwd<TX, TY, E, 32 / E, 128>(a, s);
+        if (D <= 16384) return fwd<TX, TY, E, 32 / E, 512>(a, s);
+        ln_fwd_wide_kernel<TX, TY, E><<<(unsigned)a.rows, 512, 0, s>>>(a);
+    } else {
+        // a shifted row has one column more
+        const int64_t W = D + (ACCESS == PAIRS);
+        if (W <= 512) return fwd_any<TX, TY, E, 32, 256>(a, s);
+        if (W <= 1024) return fwd_any<TX, TY, E, 64, 256>(a, s);
+        if (W <= 2048) return fwd_any<TX, TY, E, 128, 256>(a, s);
+        if (W <= 4096) return fwd_any<TX, TY, E, 256, 256>(a, s);
+        if (W <= 8192) return fwd_any<TX, TY, E, 512, 512>(a, s);
+        ln_fwd_wide_kernel<TX, TY, 1><<<(unsigned)a.rows, 512, 0, s>>>(a);
+    }
+}
+
+template <typename TX, typename TY, int E, int NC, int T>
+int bwd(const NormArgs &a, cudaStream_t s) {
+    constexpr int NT = 512, G = NT / T, W = T * NC * E;
+    int64_t blocks = div_up(a.rows, G);
+    blocks += blocks & 1;
+    if (blocks > bwd_blocks()) blocks = bwd_blocks();
+    const size_t smem = (size_t)(4 + W + 4 + (a.part ? G / 2 * 2 * W : 0)) * sizeof(float);
+    const auto kern = ln_bwd_kernel<TX, TY, E, NC, T, NT>;
+    if (smem > 40 * 1024) cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    kern<<<(unsigned)blocks, NT, smem, s>>>(a);
+    return (int)blocks;
 }
 
 // Returns the number of partial rows written.
-template <typename TX, typename TY, bool VEC>
+template <typename TX, typename TY, int ACCESS>
 int bwd_rows(const NormArgs &a, cudaStream_t s) {
-    constexpr int E = !VEC ? 1 : (sizeof(TX) == 4 && sizeof(TY) == 4 ? 4 : 8);
-    const int64_t D = a.cols;
-    const int most = BWD_BLOCKS_PER_SM * sm_count();
-    const int b4 = (int)(div_up(a.rows, 4) < most ? div_up(a.rows, 4) : most);
-    const int b1 = (int)(a.rows < most ? a.rows : most);
-    if (D <= 256) return bwd<TX, TY, E, 8 / E, 32, 128>(a, b4, s);
-    if (D <= 1024) return bwd<TX, TY, E, 32 / E, 32, 128>(a, b4, s);
-    if (D <= 4096) return bwd<TX, TY, E, 32 / E, 128, 128>(a, b1, s);
-    if (D <= 8192) return bwd<TX, TY, E, 16 / E, 512, 512>(a, b1, s);
+    constexpr int E = ACCESS == SINGLE ? 1 : ACCESS == PAIRS ? 2 : sizeof(TX) == 4 && sizeof(TY) == 4 ? 4 : 8;
+    const int64_t D = a.cols, W = D + (ACCESS == PAIRS);
+    if (W <= 256) return bwd<TX, TY, E, 8 / E, 32>(a, s);
+    if (W <= 512) return bwd<TX, TY, E, 16 / E, 32>(a, s);
+    if (W <= 1024) return bwd<TX, TY, E, 16 / E, 64>(a, s);
+    if (W <= 2048) return bwd<TX, TY, E, 16 / E, 128>(a, s);
+    if (W <= 4096) return bwd<TX, TY, E, 16 / E, 256>(a, s);
+    if (W <= 8192) return bwd<TX, TY, E, 16 / E, 512>(a, s);
     int n = 0;
     if (a.part) {
         const int64_t cb = div_up(D, 32);
         int64_t chunks = div_up(4 * sm_count(), cb);
         if (chunks > div_up(a.rows, 8)) chunks = div_up(a.rows, 8);
-        n = (int)(chunks < most ? chunks : most);
+        n = (int)(chunks < bwd_blocks() ? chunks : bwd_blocks());
         ln_bwd_wide_cols_kernel<TX, TY><<<dim3((unsigned)cb, (unsigned)n), 256, 0, s>>>(a);
     }
-    if (a.y) ln_bwd_wide_dx_kernel<TX, TY, E><<<(unsigned)a.rows, 512, 0, s>>>(a);
+    constexpr int EW = ACCESS == VEC ? E : 1;
+    if (a.y) ln_bwd_wide_dx_kernel<TX, TY, EW><<<(unsigned)a.rows, 512, 0, s>>>(a);
     return n;
 }
 
+template <int A>
+using AccessC = std::integral_constant<int, A>;
+
 template <typename F>
-int by_types(int xt, int yt, bool vec, const F &f) {
+int by_types(int xt, int yt, Access access, const F &f) {
     using bf = __nv_bfloat16;
-#define SC_PAIR(a, b, A, B)                          \
-    if (xt == a && yt == b) return vec ? f((A *)nullptr, (B *)nullptr, std::true_type()) \
-                                       : f((A *)nullptr, (B *)nullptr, std::false_type());
-    SC_PAIR(SC_F32, SC_F32, float, float)
-    SC_PAIR(SC_F32, SC_BF16, float, bf)
-    SC_PAIR(SC_F32, SC_F16, float, __half)
-    SC_PAIR(SC_BF16, SC_F32, bf, float)
-    SC_PAIR(SC_BF16, SC_BF16, bf, bf)
-    SC_PAIR(SC_F16, SC_F32, __half, float)
-    SC_PAIR(SC_F16, SC_F16, __half, __half)
-#undef SC_PAIR
-    return 0;
+    auto with = [&](auto *x, auto *y) {
+        if (access == VEC) return f(x, y, AccessC<VEC>());
+        if (access == PAIRS) return f(x, y, AccessC<PAIRS>());
+        return f(x, y, AccessC<SINGLE>());
+    };
+    if (xt == SC_F32 && yt == SC_F32) return with((float *)nullptr, (float *)nullptr);
+    if (xt == SC_F32 && yt == SC_BF16) return with((float *)nullptr, (bf *)nullptr);
+    if (xt == SC_F32) return with((float *)nullptr, (__half *)nullptr);
+    if (xt == SC_BF16 && yt == SC_F32) return with((bf *)nullptr, (float *)nullptr);
+    if (xt == SC_BF16) return with((bf *)nullptr, (bf *)nullptr);
+    if (yt == SC_F32) return with((__half *)nullptr, (float *)nullptr);
+    return with((__half *)nullptr, (__half *)nullptr);
 }
 
 int check_desc(const sc_norm_desc *d, const char *who) {
@@ -475,24 +674,44 @@ int check_ld(int64_t ld, int64_t cols, const char *who, const char *name) {
     return SC_ERR_ARG;
 }
 
-// Columns of one vector access, and whether a matrix allows it on every row.
-int vec_of(const sc_norm_desc &d) { return d.x_type == SC_F32 && d.y_type == SC_F32 ? 4 : 8; }
-bool vec_ok(const sc_norm_desc &d, const void *p, int64_t ld) {
-    return !p || (aligned16(p) && ld % vec_of(d) == 0);
+struct Matrix {
+    const void *p;
+    int64_t ld;
+    int type;
+};
+
+Access access_of(const sc_norm_desc &d, const void *weight, const void *bias, std::initializer_list<Matrix> ms) {
+    const int e = d.x_type == SC_F32 && d.y_type == SC_F32 ? 4 : 8;
+    bool vec = d.cols % e == 0 && aligned16(weight) && aligned16(bias), pairs = true;
+    for (const Matrix &m : ms) {
+        if (!m.p) continue;
+        vec = vec && aligned16(m.p) && m.ld % e == 0;
+        // pairs begin on the same columns in every matrix
+        pairs = pairs && reinterpret_cast<uintptr_t>(m.p) % (2 * type_size(m.type)) == 0 && (m.ld & 1) == (ms.begin()->ld & 1);
+    }
+    return vec ? VEC : pairs ? PAIRS : SINGLE;
 }
 
 int64_t bwd_workspace(const sc_norm_desc &d) {
-    const int64_t most = (int64_t)BWD_BLOCKS_PER_SM * sm_count();
-    return round_up((d.rows < most ? d.rows : most) * 2 * d.cols * (int64_t)sizeof(float), 256);
+    const int64_t most = bwd_blocks(), rows = d.rows + (d.rows & 1);
+    return round_up((rows < most ? rows : most) * 2 * d.cols * (int64_t)sizeof(float), 256);
 }
 
 }  // namespace
 
 int launch_finish_columns(const float *part, int n_part, int n_out, int64_t cols, void *out0,
                           void *out1, int out_type, cudaStream_t stream) {
-    finish_columns_kernel<<<(unsigned)div_up(n_out * cols, 32), 512, 0, stream>>>(
-        part, n_part, n_out, cols, out0, out1, out_type);
-    const cudaError_t e = cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];  // begins under the kernel that writes the partial rows
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)div_up(n_out * cols, 32));
+    cfg.blockDim = dim3(512);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, finish_columns_kernel, part, n_part, n_out, cols, out0, out1, out_type);
+    if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? SC_OK : cuda_fail(e, "column sums");
 }
 
@@ -529,10 +748,9 @@ extern "C" int sc_layer_norm(const sc_norm_desc *d, const void *x, const void *w
     a.y = y;
     a.mean = mean;
     a.rstd = rstd;
-    const bool vec = d->cols % vec_of(*d) == 0 && vec_ok(*d, x, d->ld_x) && vec_ok(*d, y, d->ld_y) &&
-                     vec_ok(*d, weight, 0) && vec_ok(*d, bias, 0);
+    const Access access = access_of(*d, weight, bias, {{x, d->ld_x, d->x_type}, {y, d->ld_y, d->y_type}});
     const cudaStream_t s = (cudaStream_t)stream;
-    by_types(d->x_type, d->y_type, vec, [&](auto *tx, auto *ty, auto v) {
+    by_types(d->x_type, d->y_type, access, [&](auto *tx, auto *ty, auto v) {
         fwd_rows<std::remove_pointer_t<decltype(tx)>, std::remove_pointer_t<decltype(ty)>, decltype(v)::value>(a, s);
         return 0;
     });
@@ -595,10 +813,10 @@ extern "C" int sc_layer_norm_backward(const sc_norm_desc *d, const void *dy, con
     const cudaStream_t s = (cudaStream_t)stream;
     int n_part = 0;
     if (d->rows > 0) {
-        const bool vec = d->cols % vec_of(*d) == 0 && vec_ok(*d, x, d->ld_x) &&
-                         vec_ok(*d, dy, d->ld_y) && vec_ok(*d, dx, d->ld_dx) &&
-                         vec_ok(*d, a.add, d->ld_add) && vec_ok(*d, weight, 0);
-        n_part = by_types(d->x_type, d->y_type, vec, [&](auto *tx, auto *ty, auto v) {
+        const Access access = access_of(*d, nullptr, nullptr,
+                                        {{x, d->ld_x, d->x_type}, {dy, d->ld_y, d->y_type},
+                                         {dx, d->ld_dx, d->x_type}, {a.add, d->ld_add, d->x_type}});
+        n_part = by_types(d->x_type, d->y_type, access, [&](auto *tx, auto *ty, auto v) {
             return bwd_rows<std::remove_pointer_t<decltype(tx)>, std::remove_pointer_t<decltype(ty)>, decltype(v)::value>(a, s);
         });
         const cudaError_t e = cudaGetLastError();
