@@ -74,25 +74,43 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     return d;
 }
 
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
 // gelu(z) = z Phi(z) without special functions, for the matrix product's
 // epilogue: its few warps would wait for them (16 a clock and SM).  For |z| <=
-// 5.25, Phi(z) = 1/2 + z P(z^2) with a polynomial of degree 13 in t = 2 z^2 /
+// 5.25, Phi(z) = 1/2 + z P(t) with a polynomial of degree 13 in t = 2 z^2 /
 // 5.25^2 - 1 (least squares at Chebyshev nodes, weights adjusted towards equal
-// ripples: off by 0.8e-7, with fp32 roundings 1.7e-7); beyond, Phi is within
-// 0.8e-7 of 0 and 1.  The result is off by at most 4 * 2^-24 |z|.
+// ripples: off by 0.8e-7, with fp32 roundings 1.7e-7).  Beyond, t stays 1, so
+// 1/2 + z P(1) leaves [0, 1] and saturates to Phi's limits.  The result is off
+// by at most 4 * 2^-24 |z|.
 __device__ __forceinline__ float2 gelu2(float2 z) {
     constexpr float A = 5.25f;
     constexpr float P[14] = {1.346593648e-01f,  -6.712665409e-02f, 4.964389279e-02f,  -3.976862878e-02f, 3.206431866e-02f,
                              -2.499500290e-02f, 1.832570881e-02f,  -1.295403950e-02f, 9.071036242e-03f,  -5.120746791e-03f,
                              1.868756372e-03f,  -1.325572259e-03f, 1.456877217e-03f,  -5.612471141e-04f};
-    const float2 c = make_float2(fminf(fmaxf(z.x, -A), A), fminf(fmaxf(z.y, -A), A));
-    const float2 s = fma2(c, c, make_float2(0.f, 0.f));
-    const float2 t = fma2(s, make_float2(2.f / (A * A), 2.f / (A * A)), make_float2(-1.f, -1.f));
+    float2 t = fma2(mul2(z, z), make_float2(2.f / (A * A), 2.f / (A * A)), make_float2(-1.f, -1.f));
+    t = make_float2(fminf(t.x, 1.f), fminf(t.y, 1.f));
     float2 h = make_float2(P[13], P[13]);
 #pragma unroll
     for (int i = 12; i >= 0; --i) h = fma2(h, t, make_float2(P[i], P[i]));
-    const float2 f = fma2(c, h, make_float2(0.5f, 0.5f));
-    return make_float2(z.x * (z.x <= -A ? 0.f : f.x), z.y * (z.y <= -A ? 0.f : f.y));
+    return mul2(z, make_float2(__saturatef(fmaf(z.x, h.x, 0.5f)), __saturatef(fmaf(z.y, h.y, 0.5f))));
 }
 
 template <int ACT>

@@ -276,7 +276,11 @@ __device__ __forceinline__ void epilogue_rows(const GemmArgs &p, float (&v)[R][8
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[r][i] += b[i];
+            for (int i = 0; i < 8; i += 2) {
+                const float2 z = add2(make_float2(v[r][i], v[r][i + 1]), make_float2(b[i], b[i + 1]));
+                v[r][i] = z.x;
+                v[r][i + 1] = z.y;
+            }
     }
     if (p.pre) store_rows_any<R>(q.pre, p.pre_type, step * p.ld_pre, in, v);
     if constexpr (ACT != SC_ACT_NONE) {
