@@ -224,13 +224,6 @@ __device__ __forceinline__ void epilogue1(const GemmArgs &p, float z, float bias
 
 // 8 columns of R rows, `step` elements apart, from p on.
 template <typename T, int R>
-__device__ __forceinline__ void load_rows(const void *p, int64_t step, const bool (&in)[R], float (&v)[R][8]) {
-    const T *q = static_cast<const T *>(p);
-#pragma unroll
-    for (int r = 0; r < R; ++r, q += step)
-        if (in[r]) load_vec<T, 8>(q, v[r]);
-}
-template <typename T, int R>
 __device__ __forceinline__ void store_rows(void *p, int64_t step, const bool (&in)[R], const float (&v)[R][8]) {
     T *q = static_cast<T *>(p);
 #pragma unroll
@@ -259,19 +252,62 @@ __device__ __forceinline__ RowPtrs row_ptrs(const GemmArgs &p, int64_t row, int 
             at_element(p.res, p.out_type, row * p.ld_res + col)};
 }
 
-// Epilogue of 8 columns (their bias: b) of R rows from q on, `step` rows apart;
-// in: the row exists.  Every step runs over all of them before the next one
-// begins: the few warps of an epilogue hide latency by independent work, not
-// by each other.
-template <int ACT, int R>
-__device__ __forceinline__ void epilogue_rows(const GemmArgs &p, float (&v)[R][8], const float (&b)[8], const RowPtrs &q,
-                                              int step, const bool (&in)[R]) {
-    float a[R][8];
-    if (p.res) {
-        if (p.out_type == SC_F32) load_rows<float, R>(q.res, step * p.ld_res, in, a);
-        else if (p.out_type == SC_BF16) load_rows<__nv_bfloat16, R>(q.res, step * p.ld_res, in, a);
-        else load_rows<__half, R>(q.res, step * p.ld_res, in, a);
+// What a kernel knows of the result's type.
+enum { OUT_ANY, OUT_F32, OUT_16 };
+template <int OUT>
+__device__ __forceinline__ bool out_f32(const GemmArgs &p) {
+    return OUT == OUT_F32 || (OUT == OUT_ANY && p.out_type == SC_F32);
+}
+
+// R rows' 8 columns of the residual, as it lies in memory: loaded ahead of
+// their use without taking more registers than bytes.
+template <int R, int OUT>
+struct Residual {
+    static constexpr int Q = OUT == OUT_16 ? 1 : 2;
+    uint4 w[R][Q];
+    __device__ __forceinline__ void load(const GemmArgs &p, const char *q, int64_t step_bytes, const bool (&in)[R]) {
+#pragma unroll
+        for (int r = 0; r < R; ++r, q += step_bytes)
+            if (in[r]) {
+                w[r][0] = reinterpret_cast<const uint4 *>(q)[0];
+                if (Q == 2 && out_f32<OUT>(p)) w[r][Q - 1] = reinterpret_cast<const uint4 *>(q)[1];
+            }
     }
+    template <typename T>
+    __device__ __forceinline__ void add(float (&v)[R][8]) const {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const uint4 l = w[r][0], h = w[r][Q - 1];
+            const uint32_t k[8] = {l.x, l.y, l.z, l.w, h.x, h.y, h.z, h.w};
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                float x, y;
+                if constexpr (sizeof(T) == 4) {
+                    x = __uint_as_float(k[i]);
+                    y = __uint_as_float(k[i + 1]);
+                } else {
+                    unpack2<T>(k[i / 2], x, y);
+                }
+                const float2 z = add2(make_float2(v[r][i], v[r][i + 1]), make_float2(x, y));
+                v[r][i] = z.x;
+                v[r][i + 1] = z.y;
+            }
+        }
+    }
+    __device__ __forceinline__ void add_to(const GemmArgs &p, float (&v)[R][8]) const {
+        if (Q == 2 && out_f32<OUT>(p)) add<float>(v);
+        else if (p.out_type == SC_BF16) add<__nv_bfloat16>(v);
+        else add<__half>(v);
+    }
+};
+
+// Epilogue of 8 columns (their bias: b) of R rows from q on, `step` rows apart;
+// in: the row exists; a: their residual.  Every step runs over all of them
+// before the next one begins: the few warps of an epilogue hide latency by
+// independent work, not by each other.
+template <int ACT, int OUT, int R>
+__device__ __forceinline__ void epilogue_rows(const GemmArgs &p, float (&v)[R][8], const float (&b)[8],
+                                              const Residual<R, OUT> &a, const RowPtrs &q, int step, const bool (&in)[R]) {
     if (p.bias) {
 #pragma unroll
         for (int r = 0; r < R; ++r)
@@ -298,13 +334,10 @@ __device__ __forceinline__ void epilogue_rows(const GemmArgs &p, float (&v)[R][8
                 }
             }
     }
-    if (p.res) {
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[r][i] += a[r][i];
-    }
-    store_rows_any<R>(q.out, p.out_type, step * p.ld_out, in, v);
+    if (p.res) a.add_to(p, v);
+    if (out_f32<OUT>(p)) store_rows<float, R>(q.out, step * p.ld_out, in, v);
+    else if (p.out_type == SC_BF16) store_rows<__nv_bfloat16, R>(q.out, step * p.ld_out, in, v);
+    else store_rows<__half, R>(q.out, step * p.ld_out, in, v);
 }
 
 // tcgen05.ld without its wait; the registers are valid after tmem_wait_ld.
@@ -409,25 +442,41 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
             const int at = ((j & 1) * 8 + (j >> 1)) ^ (lane & 7);
             *reinterpret_cast<float4 *>(stg + lane * STG_COLS + at * 4) = make_float4(a, b, c, d);
         };
-        auto store_staged = [&](int64_t row0, int col0) {
+        constexpr int R = 4;  // rows of a lane at a time: lr + 4 k
+        constexpr int OUT = SPLIT ? OUT_ANY : KEEP ? OUT_F32 : OUT_16;
+        // 16-bit residuals are loaded one step ahead; fp32 ones (and the sums
+        // beside them) would take too many registers
+        constexpr bool AHEAD = !KEEP;
+        Residual<R, OUT> ahead;
+        const int64_t res_row = p.ld_res * (p.out_type == SC_F32 ? 4 : 2);
+        auto rows_in = [&](int64_t row, bool (&in)[R]) {
+#pragma unroll
+            for (int k = 0; k < R; ++k) in[k] = row + 4 * k < p.M;
+        };
+        // the residual of the lane's first rows of the 64 columns from col0 on
+        auto fetch_first = [&](int64_t row0, int col0) {
+            if (AHEAD && p.vec && p.res && col0 + lc * 8 < p.N) {
+                bool in[R];
+                rows_in(row0 + lr, in);
+                ahead.load(p, row_ptrs(p, row0 + lr, col0 + lc * 8).res, 4 * res_row, in);
+            }
+        };
+        // more: another 64 columns follow
+        auto store_staged = [&](int64_t row0, int col0, const float (&b)[8], bool more) {
             __syncwarp();
             if (p.vec) {
                 const int col = col0 + lc * 8;
                 if (col < p.N) {
-                    float b[8] = {};
-                    if (p.bias) load_any<8>(p.bias, p.bias_type, col, b);
-                    constexpr int R = 4;
                     RowPtrs q = row_ptrs(p, row0 + lr, col);
                     const int64_t out_step = 4 * R * p.ld_out * (p.out_type == SC_F32 ? 4 : 2);
-                    const int64_t res_step = 4 * R * p.ld_res * (p.out_type == SC_F32 ? 4 : 2);
                     const int64_t pre_step = 4 * R * p.ld_pre * (p.pre_type == SC_F32 ? 4 : 2);
-                    const int rows = (int)min((int64_t)32, p.M - row0);
                     // the same quads for rows r and r + 8
                     const float *s0 = stg + lr * STG_COLS + (lc ^ lr) * 4, *s1 = stg + (lr + 4) * STG_COLS + (lc ^ (lr + 4)) * 4;
 #pragma unroll 1
                     for (int r = lr; r < 32; r += 4 * R) {
                         float o[R][8];
                         bool in[R];
+                        rows_in(row0 + r, in);
 #pragma unroll
                         for (int k = 0; k < R; ++k) {
                             const float *f = (k & 1 ? s1 : s0) + (k >> 1) * 8 * STG_COLS;
@@ -435,13 +484,28 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
                             const float4 y = *reinterpret_cast<const float4 *>(f + 32);
                             o[k][0] = x.x; o[k][1] = x.y; o[k][2] = x.z; o[k][3] = x.w;
                             o[k][4] = y.x; o[k][5] = y.y; o[k][6] = y.z; o[k][7] = y.w;
-                            in[k] = r + 4 * k < rows;
                         }
-                        epilogue_rows<ACT, R>(p, o, b, q, 4, in);
+                        Residual<R, OUT> a;
+                        if (p.res) {
+                            if (AHEAD) {
+                                a = ahead;
+                                q.res += 4 * R * res_row;
+                                if (r + 4 * R < 32) {
+                                    bool next[R];
+                                    rows_in(row0 + r + 4 * R, next);
+                                    ahead.load(p, q.res, 4 * res_row, next);
+                                } else if (more) {
+                                    fetch_first(row0, col0 + STG_COLS);
+                                }
+                            } else {
+                                a.load(p, q.res, 4 * res_row, in);
+                                q.res += 4 * R * res_row;
+                            }
+                        }
+                        epilogue_rows<ACT, OUT, R>(p, o, b, a, q, 4, in);
                         s0 += 4 * R * STG_COLS;
                         s1 += 4 * R * STG_COLS;
                         q.out += out_step;
-                        q.res += res_step;
                         q.pre += pre_step;
                     }
                 }
@@ -460,6 +524,9 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
                 }
             }
             __syncwarp();
+        };
+        auto load_bias = [&](int col0, float (&b)[8]) {
+            if (p.vec && p.bias && col0 + lc * 8 < p.N) load_any<8>(p.bias, p.bias_type, col0 + lc * 8, b);
         };
         auto release = [&](int buf) {
             tc_fence_before();
@@ -484,6 +551,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
                         asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char *>(p.res) +
                                                                      ((row0 + lane) * p.ld_res + n0 + c) * size));
             }
+            if (!SPLIT) fetch_first(row0, n0);
             const uint32_t lane_acc = tmem + c_lo + ((uint32_t)(quad * 32) << 16);
             if constexpr (KEEP) {
                 // add up the chunks: this lane's row, columns c_lo .. c_lo + half
@@ -514,10 +582,12 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
 #pragma unroll
                     for (int c = 0; c < COLS; c += STG_COLS) {
                         if (c >= half) break;
+                        float b[8] = {};
+                        load_bias(n0 + c, b);
 #pragma unroll
                         for (int j = 0; j < STG_COLS / 4; ++j)
                             stage_quad(j, v[c + 4 * j], v[c + 4 * j + 1], v[c + 4 * j + 2], v[c + 4 * j + 3]);
-                        store_staged(row0, n0 + c);
+                        store_staged(row0, n0 + c, b, c + STG_COLS < half);
                     }
                 }
             } else {
@@ -526,6 +596,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
                 ++n;
                 tc_fence_after();
                 for (int c = 0; c < half; c += STG_COLS) {
+                    float b[8] = {};
+                    load_bias(n0 + c, b);
                     uint32_t r[2][32];
                     tmem_ld32_async(lane_acc + buf * ACC_COLS + c, r[0]);
                     tmem_ld32_async(lane_acc + buf * ACC_COLS + c + 32, r[1]);
@@ -538,7 +610,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
                             stage_quad(k * 8 + j, __uint_as_float(r[k][4 * j]), __uint_as_float(r[k][4 * j + 1]),
                                        __uint_as_float(r[k][4 * j + 2]), __uint_as_float(r[k][4 * j + 3]));
                     if (c + STG_COLS >= half) release(buf);
-                    store_staged(row0, n0 + c);
+                    store_staged(row0, n0 + c, b, c + STG_COLS < half);
                 }
             }
         }
@@ -707,7 +779,10 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
 #pragma unroll
                     for (int j = 0; j < 8; ++j) o[0][j] = v[j];
                     const bool in[1] = {true};
-                    epilogue_rows<ACT, 1>(p, o, b, row_ptrs(p, m0 + r, n0 + c), 0, in);
+                    const RowPtrs q = row_ptrs(p, m0 + r, n0 + c);
+                    Residual<1, OUT_ANY> a;
+                    if (p.res) a.load(p, q.res, 0, in);
+                    epilogue_rows<ACT, OUT_ANY, 1>(p, o, b, a, q, 0, in);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
