@@ -51,15 +51,6 @@ int launch_gemm(int64_t M, int64_t N, int64_t K, int type16, const GemmOperand &
 // few of exp where the result is far below |n|) stay under 2^-21 |n|.
 __device__ __forceinline__ float times_sigmoid(float n, float x) { return __fdividef(n, 1.f + __expf(-x)); }
 
-// q(a) = (1 - erf(a / sqrt 2)) / 2 for a >= 0 by the rational approximation 7.1.26 of
-// Abramowitz and Stegun, Handbook of Mathematical Functions (error below
-// 0.75e-7); it shares exp(-a^2 / 2) with gelu's derivative Phi(z) + z phi(z).
-__device__ __forceinline__ float normal_tail(float a, float e) {  // e = exp(-a^2 / 2)
-    const float t = __fdividef(1.f, 1.f + 0.231641888f * a);     // 0.3275911 / sqrt 2
-    const float s = t * (0.127414796f + t * (-0.142248368f + t * (0.7107068705f + t * (-0.7265760135f + t * 0.5307027145f))));
-    return s * e;
-}
-
 // sqrt(8 / pi) (z + 0.044715 z^3): gelu_tanh is z sigmoid of it
 __device__ __forceinline__ float gelu_tanh_arg(float z) { return 1.59576912f * z * (1.f + 0.044715f * z * z); }
 
@@ -93,26 +84,38 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return d;
 }
 
-// gelu(z) = z Phi(z) without special functions, for the matrix product's
-// epilogue: its few warps would wait for them (16 a clock and SM).  For |z| <=
-// 5.25, Phi(z) = 1/2 + z P(t) with a polynomial of degree 13 in t = 2 z^2 /
+// Phi, the normal distribution's function, without special functions (16 a
+// clock and SM: an epilogue's few warps would wait for them).  z2 = z^2.  For
+// |z| <= 5.25, Phi(z) = 1/2 + z P(t) with a polynomial of degree 13 in t = 2 z^2 /
 // 5.25^2 - 1 (least squares at Chebyshev nodes, weights adjusted towards equal
 // ripples: off by 0.8e-7, with fp32 roundings 1.7e-7).  Beyond, t stays 1, so
-// 1/2 + z P(1) leaves [0, 1] and saturates to Phi's limits.  The result is off
-// by at most 4 * 2^-24 |z|.
-__device__ __forceinline__ float2 gelu2(float2 z) {
+// 1/2 + z P(1) leaves [0, 1] and saturates to Phi's limits.
+__device__ __forceinline__ float2 normal2(float2 z, float2 z2) {
     constexpr float A = 5.25f;
     constexpr float P[14] = {1.346593648e-01f,  -6.712665409e-02f, 4.964389279e-02f,  -3.976862878e-02f, 3.206431866e-02f,
                              -2.499500290e-02f, 1.832570881e-02f,  -1.295403950e-02f, 9.071036242e-03f,  -5.120746791e-03f,
                              1.868756372e-03f,  -1.325572259e-03f, 1.456877217e-03f,  -5.612471141e-04f};
-    float2 t = fma2(mul2(z, z), make_float2(2.f / (A * A), 2.f / (A * A)), make_float2(-1.f, -1.f));
+    float2 t = fma2(z2, make_float2(2.f / (A * A), 2.f / (A * A)), make_float2(-1.f, -1.f));
     t = make_float2(fminf(t.x, 1.f), fminf(t.y, 1.f));
     float2 h = make_float2(P[13], P[13]);
 #pragma unroll
     for (int i = 12; i >= 0; --i) h = fma2(h, t, make_float2(P[i], P[i]));
-    return mul2(z, make_float2(__saturatef(fmaf(z.x, h.x, 0.5f)), __saturatef(fmaf(z.y, h.y, 0.5f))));
+    return make_float2(__saturatef(fmaf(z.x, h.x, 0.5f)), __saturatef(fmaf(z.y, h.y, 0.5f)));
 }
 
+// gelu(z) = z Phi(z), off by at most 4 * 2^-24 |z|.
+__device__ __forceinline__ float2 gelu2(float2 z) { return mul2(z, normal2(z, mul2(z, z))); }
+
+// gelu'(z) = Phi(z) + z exp(-z^2 / 2) / sqrt(2 pi); the second term is 0 from
+// |z| = 16 on, which keeps infinity * 0 out.
+__device__ __forceinline__ float2 gelu_grad2(float2 z) {
+    const float2 z2 = mul2(z, z);
+    const float2 e = make_float2(__expf(-0.5f * z2.x), __expf(-0.5f * z2.y));
+    const float2 c = make_float2(fminf(fmaxf(z.x, -16.f), 16.f), fminf(fmaxf(z.y, -16.f), 16.f));
+    return fma2(mul2(c, make_float2(0.39894228f, 0.39894228f)), e, normal2(z, z2));
+}
+
+// Activations of one value.
 template <int ACT>
 __device__ __forceinline__ float act_fn(float z) {
     if constexpr (ACT == SC_ACT_RELU) return z < 0.f ? 0.f : z;  // keeps a NaN
@@ -125,11 +128,7 @@ __device__ __forceinline__ float act_fn(float z) {
 template <int ACT>
 __device__ __forceinline__ float act_grad(float z) {
     if constexpr (ACT == SC_ACT_RELU) return z > 0.f ? 1.f : (z == z ? 0.f : z);
-    if constexpr (ACT == SC_ACT_GELU) {
-        const float a = fminf(fabsf(z), 16.f), e = __expf(-0.5f * a * a), q = normal_tail(a, e);
-        const float d = (z < 0.f ? q : 1.f - q) + (z < 0.f ? -a : a) * 0.39894228f * e;
-        return z == z ? d : z;
-    }
+    if constexpr (ACT == SC_ACT_GELU) return gelu_grad2(make_float2(z, z)).x;
     if constexpr (ACT == SC_ACT_GELU_TANH) {
         const float q = times_sigmoid(1.f, gelu_tanh_arg(z));
         return q + z * q * (1.f - q) * 1.59576912f * (1.f + 0.134145f * z * z);
@@ -139,6 +138,22 @@ __device__ __forceinline__ float act_grad(float z) {
         return q * (1.f + z * (1.f - q));
     }
     return 1.f;
+}
+
+// v times the activation's derivative at z, E values.
+template <int ACT, int E>
+__device__ __forceinline__ void times_act_grad(float (&v)[E], const float (&z)[E]) {
+    if constexpr (ACT == SC_ACT_GELU && E % 2 == 0) {
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+            const float2 g = mul2(make_float2(v[e], v[e + 1]), gelu_grad2(make_float2(z[e], z[e + 1])));
+            v[e] = g.x;
+            v[e + 1] = g.y;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] *= act_grad<ACT>(z[e]);
+    }
 }
 
 }  // namespace scb

@@ -74,10 +74,7 @@ __device__ __forceinline__ void run_job(const PassJob &p, int block, float (*sum
                     if constexpr (ACT != SC_ACT_NONE) z[e] = col(e) < p.cols ? to_f(pre[col(e)]) : 0.f;
                 }
             }
-            if constexpr (ACT != SC_ACT_NONE) {
-#pragma unroll
-                for (int e = 0; e < E; ++e) v[e] *= act_grad<ACT>(z[e]);
-            }
+            if constexpr (ACT != SC_ACT_NONE) times_act_grad<ACT, E>(v, z);
 #pragma unroll
             for (int e = 0; e < E; ++e) s[e] += v[e];
             if constexpr (OUT == OUT_COPY) {
