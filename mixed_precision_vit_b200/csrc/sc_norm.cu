@@ -402,10 +402,14 @@ __global__ void __launch_bounds__(NT, 1) ln_bwd_kernel(const NormArgs p) {
         }
     }
     if (!p.part) return;
-    // Columns by number, so that groups of either shift add up.  Each column
-    // belongs to one thread of a group, and a barrier separates the steps.
+    // Aligned rows: by thread, without bank conflicts.  Pairs: by column, since
+    // groups of either shift add up; each column belongs to one thread of a
+    // group, and a barrier separates the steps.
     constexpr int W = T * NC * E;
+    constexpr bool BY_THREAD = E >= 4;
     float *slices = smem + 4 + W + 4;
+    auto at = [&](int c, int e) { return BY_THREAD ? (c * E + e) * T + t : (c * T + t) * E - shift + e; };
+    auto inside = [&](int c, int e) { return BY_THREAD || (at(c, e) >= 0 && at(c, e) < D); };
 #pragma unroll
     for (int half = G / 2; half >= 1; half /= 2) {
         if (g >= half && g < 2 * half) {
@@ -413,13 +417,11 @@ __global__ void __launch_bounds__(NT, 1) ln_bwd_kernel(const NormArgs p) {
 #pragma unroll
             for (int c = 0; c < NC; ++c)
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const int col = (c * T + t) * E - shift + e;
-                    if (col >= 0 && col < D) {
-                        s[col] = dw[c][e];
-                        s[W + col] = db[c][e];
+                for (int e = 0; e < E; ++e)
+                    if (inside(c, e)) {
+                        s[at(c, e)] = dw[c][e];
+                        s[W + at(c, e)] = db[c][e];
                     }
-                }
         }
         __syncthreads();
         if (g < half) {
@@ -427,28 +429,33 @@ __global__ void __launch_bounds__(NT, 1) ln_bwd_kernel(const NormArgs p) {
 #pragma unroll
             for (int c = 0; c < NC; ++c)
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const int col = (c * T + t) * E - shift + e;
-                    if (col >= 0 && col < D) {
-                        dw[c][e] += s[col];
-                        db[c][e] += s[W + col];
+                for (int e = 0; e < E; ++e)
+                    if (inside(c, e)) {
+                        dw[c][e] += s[at(c, e)];
+                        db[c][e] += s[W + at(c, e)];
                     }
-                }
         }
         __syncthreads();
     }
     if (g != 0) return;
     float *out = p.part + (int64_t)blockIdx.x * 2 * D;
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int col = (c * T + t) * E - shift + e;
-            if (col >= 0 && col < D) {
-                out[col] = dw[c][e];
-                out[D + col] = db[c][e];
+    for (int c = 0; c < NC; ++c) {
+        const int col = (c * T + t) * E - shift;
+        if constexpr (BY_THREAD) {
+            if (col < D) {  // D is a multiple of E: both rows are aligned
+                store_vec<float, E>(out + col, dw[c]);
+                store_vec<float, E>(out + D + col, db[c]);
             }
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (col + e >= 0 && col + e < D) {
+                    out[col + e] = dw[c][e];
+                    out[D + col + e] = db[c][e];
+                }
         }
+    }
 }
 
 // Backward of rows too wide for registers: dx by one block per row in two
