@@ -274,12 +274,20 @@ __global__ void __launch_bounds__(NT) ln_fwd_any_kernel(const NormArgs p) {
             b[c][e] = param(p.b, p.w_type, col, D, 0.f);
         }
     const float inv = 1.f / (float)D;
+    Raw<TX, E> next[NC];  // the next row, loaded while the current one is worked on
+    auto fetch = [&](int64_t row) {
+        if (row >= p.rows) return;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+            next[c].load(static_cast<const TX *>(p.x) + row * p.ld_x, (c * T + t) * E - shift, D);
+    };
+    fetch(first);
     for (int64_t row = first; row < p.rows; row += step) {
-        const TX *x = static_cast<const TX *>(p.x) + row * p.ld_x;
         float v[NC][E];
         float s = 0.f, unused = 0.f;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) load_cols<TX, E>(x, (c * T + t) * E - shift, D, v[c], 0.f);
+        for (int c = 0; c < NC; ++c) next[c].get(v[c]);
+        fetch(row + step);
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
