@@ -149,7 +149,7 @@ int launch_gemm(int64_t M, int64_t N, int64_t K, int type16, const GemmOperand &
     p.n_prod = a.planes == 3 ? 6 : 1;
     p.n_k = (int)div_up(K, GK);
     const Shape sh = choose(M, N, p.n_k * p.n_prod);
-    p.chunk = epi.out_type == SC_F32 ? CHUNK : p.n_k * p.n_prod;
+    p.chunk = epi.out_type == SC_F32 || sh.parts > 1 ? CHUNK : p.n_k * p.n_prod;
     p.bn = sh.bn;
     p.M = (int)M;
     p.N = (int)N;

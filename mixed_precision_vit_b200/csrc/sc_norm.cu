@@ -637,8 +637,9 @@ int bwd_rows(const NormArgs &a, cudaStream_t s) {
         n = (int)(chunks < bwd_blocks() ? chunks : bwd_blocks());
         ln_bwd_wide_cols_kernel<TX, TY><<<dim3((unsigned)cb, (unsigned)n), 256, 0, s>>>(a);
     }
-    constexpr int EW = ACCESS == VEC ? E : 1;
-    if (a.y) ln_bwd_wide_dx_kernel<TX, TY, EW><<<(unsigned)a.rows, 512, 0, s>>>(a);
+    // the weight is read like the rows here, so it must be aligned like them
+    if (a.y && ACCESS == VEC && aligned16(a.w)) ln_bwd_wide_dx_kernel<TX, TY, E><<<(unsigned)a.rows, 512, 0, s>>>(a);
+    else if (a.y) ln_bwd_wide_dx_kernel<TX, TY, 1><<<(unsigned)a.rows, 512, 0, s>>>(a);
     return n;
 }
 

@@ -289,6 +289,12 @@ def _scratch(desc, need: int, workspace, like: torch.Tensor):
     return workspace
 
 
+def _status(t, dev: int):
+    if t is not None and (t.dtype != torch.int32 or t.get_device() != dev or t.numel() < 1):
+        raise ValueError(f"dev_status must be an int32 tensor on device {dev}")
+    return _ptr(t)
+
+
 def _act_code(act) -> int:
     if isinstance(act, str):
         try:
@@ -426,7 +432,7 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias=None, residual=None, act="none
     xp, wp = x.data_ptr(), w.data_ptr()
     ws = _scratch(d, L.check_bytes(lib.sc_linear_workspace_bytes(d, xp, wp)), workspace, x)
     L.check(lib.sc_linear(d, xp, wp, _ptr(bias), _ptr(residual), out.data_ptr(), _ptr(pre),
-                          _ptr(dev_status), _raw_stream(dev)))
+                          _status(dev_status, dev), _raw_stream(dev)))
     del ws
     return out, pre
 
@@ -470,7 +476,7 @@ def linear_backward(dout: torch.Tensor, x: torch.Tensor, w: torch.Tensor, pre=No
     dp, xp, wp = dout.data_ptr(), x.data_ptr(), w.data_ptr()
     ws = _scratch(d, L.check_bytes(lib.sc_linear_backward_workspace_bytes(d, dp, xp, wp)), workspace, x)
     L.check(lib.sc_linear_backward(d, dp, xp, wp, _ptr(pre) if code else None, _ptr(dx), _ptr(dw),
-                                   _ptr(db), _ptr(dev_status), _raw_stream(dev)))
+                                   _ptr(db), _status(dev_status, dev), _raw_stream(dev)))
     del ws
     return dx, dw, db
 

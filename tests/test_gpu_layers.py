@@ -7,6 +7,9 @@ d u sum|terms|; the tensor cores may cut where fp32 rounds, so there d is the
 number of terms.  Every bound is the first-order sum of the roundings on the
 way, with the counts written beside it."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -15,6 +18,7 @@ from mixed_precision_vit_b200 import _lib as L
 from mixed_precision_vit_b200 import sc
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
 U = 2.0 ** -24
 
@@ -255,6 +259,61 @@ def test_layer_norm_gradients_against_differences():
         ana = (grad.double() * v.double()).sum().item()
         lim = (2.0 ** -18 / (2 * e) + 8 * e * e / 6) * (G.abs().double().sum().item())
         assert abs(num - ana) <= lim, (k, num, ana, lim)
+
+
+@pytest.mark.parametrize("D", [64, 1000, 4096, 8200, 20000])
+@pytest.mark.parametrize("wt", [F32, BF16])
+def test_layer_norm_params_off_their_boundary(D, wt):
+    g = gen(9)
+    x, dy = rnd(g, 5, D), rnd(g, 5, D)
+    w, b = rnd(g, D + 1, dtype=wt)[1:], rnd(g, D + 3, dtype=wt)[3:]
+    _, mean, rstd = check_ln(x, w, b, F32)
+    check_lnb(dy, x, mean, rstd, w, None)
+
+
+@pytest.mark.parametrize("xt,yt", [(BF16, F32), (F32, F32), (F16, F16)])
+@pytest.mark.parametrize("D,pads", [(331, (0, 2, 4, 6)), (331, (0, 1, 0, 2)), (512, (1, 3, 5, 7)), (1023, (0, 0, 2, 2))])
+def test_layer_norm_odd_strides(D, pads, xt, yt):
+    """Strides of one parity (accesses of two elements) and of both (one element)."""
+    g = gen(10)
+    px, py, pa, po = pads
+    x, _ = strided(rnd(g, 61, D, dtype=xt), px)
+    dy, _ = strided(rnd(g, 61, D, dtype=yt), py)
+    add, _ = strided(rnd(g, 61, D, dtype=xt), pa)
+    out, big = strided(torch.zeros(61, D, dtype=yt, device="cuda"), po)
+    w, b = 1 + rnd(g, D, scale=0.2), rnd(g, D)
+    _, mean, rstd = check_ln(x, w, b, yt, out=out)
+    assert big[:, D:].isnan().all()
+    check_lnb(dy, x, mean, rstd, w, add)
+    off = torch.zeros(61 * D + 1, dtype=xt, device="cuda")[1:].view(61, D).copy_(x)
+    check_ln(off, w, b, yt)
+    check_lnb(dy, off, mean, rstd, w, off)
+
+
+def test_offsets_beyond_32_bits():
+    """Rows that start more than 2^31 elements into their buffer."""
+    g = gen(35)
+    rows, ld = 70000, 32768
+    big = torch.empty(rows, ld, dtype=BF16, device="cuda")
+    x = big[:, :72]
+    x.copy_(rnd(g, rows, 72, dtype=BF16))
+    w = rnd(g, 72)
+    tail = x[-300:].contiguous()
+    y, mean, rstd = sc.layer_norm(x, w, want_stats=True)
+    assert torch.equal(y[-300:], sc.layer_norm(tail, w)[0])
+    out = big[:, 16384:16384 + 72]
+    sc.layer_norm(x, w, out=out)
+    assert torch.equal(out, y)
+    dx, _, _ = sc.layer_norm_backward(out, x, mean, rstd, w)
+    assert torch.equal(dx[-300:], sc.layer_norm_backward(y[-300:], tail, mean[-300:], rstd[-300:], w)[0])
+    wl = rnd(g, 40, 72, dtype=BF16, scale=0.1)
+    sc.linear(x, wl, out=big[:, 8192:8192 + 40])
+    assert torch.equal(big[-300:, 8192:8192 + 40], sc.linear(tail, wl)[0])
+    dl = big[:, 8192:8192 + 40]
+    dx, dw, _ = sc.linear_backward(dl, x, wl, grad_dtype=F32)
+    assert torch.equal(dx[-300:], sc.linear_backward(dl[-300:].contiguous(), tail, wl)[0])
+    ref = dl.double().t() @ x.double()
+    close(dw, ref, (rows + 16) * U * (dl.double().abs().t() @ x.double().abs()), "dw")
 
 
 # ---- linear ----------------------------------------------------------------------------
@@ -537,6 +596,50 @@ def test_norm_feeds_the_quantiser():
     lv, s, _ = sc.quantize(y, axis=0)
     back = (lv.float() - 128) * s[..., None]
     assert ((back - y).abs() <= 0.5001 * s[..., None]).all()
+
+
+def test_first_call_inside_a_capture():
+    """A fresh process whose first calls of every layer are captured."""
+    code = """
+import sys, torch
+sys.path.insert(0, %r)
+from mixed_precision_vit_b200 import sc
+x = torch.randn(300, 72, device="cuda").bfloat16()
+w = torch.randn(40, 72, device="cuda").bfloat16()
+f = torch.randn(5, 64, device="cuda")
+lw = torch.randn(72, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+def calls():
+    y, m, r = sc.layer_norm(x, lw, want_stats=True)
+    o, pre = sc.linear(y, w, None, None, "gelu", want_pre=True)
+    dx, dw, db = sc.linear_backward(o, y, w, pre, "gelu")
+    return (y, o, dx, dw, db, *sc.layer_norm_backward(dx, x, m, r, lw), sc.linear(f, f)[0])
+with torch.cuda.graph(g):
+    held = calls()
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(held, calls()))
+print("captured")
+""" % ROOT
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+def test_two_graphs_replayed_in_turn():
+    x, p = mlp_case(36, rows=520)
+    graphs, held = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            held.append(mlp(x, p))
+        graphs.append(g)
+    ref = mlp(x, p)
+    for g in graphs + graphs[::-1]:
+        g.replay()
+    torch.cuda.synchronize()
+    for h in held:
+        assert all(torch.equal(a, b) for a, b in zip(h, ref))
 
 
 def test_streams_and_graphs():
