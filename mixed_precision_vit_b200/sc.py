@@ -275,13 +275,22 @@ class _On:
         self.dev.__exit__(*exc)
 
 
+def _new(shape, dtype, like: torch.Tensor) -> torch.Tensor:
+    """An uninitialised contiguous tensor (empty_strided is the cheapest way to one)."""
+    if len(shape) == 2:
+        return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=like.device)
+    if len(shape) == 1:
+        return torch.empty_strided(shape, (1,), dtype=dtype, device=like.device)
+    return torch.empty(shape, dtype=dtype, device=like.device)
+
+
 def _scratch(desc, need: int, workspace, like: torch.Tensor):
     """Puts a workspace of `need` bytes into the descriptor; the caller keeps the
     returned tensor until the call is enqueued."""
     if need <= 0:
         return None
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
+        workspace = _new((need,), torch.uint8, like)
     elif workspace.device != like.device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
     desc.workspace = workspace.data_ptr()
@@ -327,15 +336,15 @@ def layer_norm(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-6, *, ou
         _vector(weight, D, "weight", dev)
         wt = _type(weight.dtype, "weight")
     if out is None:
-        out = x.new_empty(shape, dtype=out_dtype or xt)
+        out = _new(shape, out_dtype or xt, x)
         ld_y = D
     else:
         ld_y = _like(out, "out", dev, shape, out_dtype)
     mean = rstd = None
     if want_stats:
         lead = (rows,) if len(shape) == 2 else shape[:-1]
-        mean = x.new_empty(lead, dtype=torch.float32)
-        rstd = x.new_empty(lead, dtype=torch.float32)
+        mean = _new(lead, torch.float32, x)
+        rstd = _new(lead, torch.float32, x)
     d = L.ScNormDesc(rows, D, ld, ld_y, 0, 0, eps, _type(xt, "x"), _type(out.dtype, "out"), wt)
     L.check(L.lib().sc_layer_norm(d, x.data_ptr(), _ptr(weight), _ptr(bias), out.data_ptr(),
                                   _ptr(mean), _ptr(rstd), _raw_stream(dev)))
@@ -375,15 +384,15 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
     else:
         pt = param_dtype or torch.float32
     ld_add = 0 if dx_add is None else _like(dx_add, "dx_add", dev, shape, xt)
-    dx = x.new_empty(shape) if want_dx else None
+    dx = _new(shape, xt, x) if want_dx else None
     dw = db = None
     d = L.ScNormDesc(rows, D, ld, ld_y, D, ld_add, 0.0, _type(xt, "x"), _type(dy.dtype, "dy"),
                      _type(pt, "weight"))
     lib = L.lib()
     ws = None
     if want_params:
-        dw = x.new_empty((D,), dtype=pt)
-        db = x.new_empty((D,), dtype=pt)
+        dw = _new((D,), pt, x)
+        db = _new((D,), pt, x)
         ws = _scratch(d, L.check_bytes(lib.sc_layer_norm_workspace_bytes(d)), workspace, x)
     L.check(lib.sc_layer_norm_backward(d, dy.data_ptr(), x.data_ptr(), _ptr(weight), mean.data_ptr(),
                                        rstd.data_ptr(), _ptr(dx_add), _ptr(dx), _ptr(dw), _ptr(db),
@@ -422,10 +431,10 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias=None, residual=None, act="none
     ld_res = 0 if residual is None else _like(residual, "residual", dev, shape, ot)
     ld_out = N
     if out is None:
-        out = x.new_empty(shape, dtype=ot)
+        out = _new(shape, ot, x)
     else:
         ld_out = _like(out, "out", dev, shape, ot)
-    pre = x.new_empty(shape) if want_pre else None
+    pre = _new(shape, xt, x) if want_pre else None
     d = L.ScLinearDesc(M, N, K, ld_x, ld_w, ld_out, ld_res, N, 0, 0, _type(xt, "x"), _type(ot, "out"),
                        bt, 0, _act_code(act))
     lib = L.lib()
@@ -467,9 +476,9 @@ def linear_backward(dout: torch.Tensor, x: torch.Tensor, w: torch.Tensor, pre=No
             raise ValueError("an activation's gradient needs pre")
         ld_pre = _like(pre, "pre", dev, shape, xt)
     gt = grad_dtype or xt
-    dx = x.new_empty(x.shape) if want_dx else None
-    dw = x.new_empty((N, K), dtype=gt) if want_dw else None
-    db = x.new_empty((N,), dtype=gt) if want_db else None
+    dx = _new(x.shape, xt, x) if want_dx else None
+    dw = _new((N, K), gt, x) if want_dw else None
+    db = _new((N,), gt, x) if want_db else None
     d = L.ScLinearDesc(M, N, K, ld_x, ld_w, ld_out, 0, ld_pre, K, K, _type(xt, "x"),
                        _type(dout.dtype, "dout"), 0, _type(gt, "grad_dtype"), code)
     lib = L.lib()
