@@ -26,7 +26,7 @@ struct GemmEpilogue {
     int bias_type, out_type, pre_type, act;
 };
 
-// Column sums left to finish: out[c] = sum_i part[i][c], i < n, in ascending i.
+// Column sums left to finish: out[c] = sum_i part[i][c], i < n.
 struct ColumnSums {
     const float *part;
     void *out;

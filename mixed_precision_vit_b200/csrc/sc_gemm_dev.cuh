@@ -54,7 +54,10 @@ constexpr int CHUNK = 16;               // stages (1024 indexes) per accumulatio
 // permuted so that both a lane's row (written) and 8 lanes' row (read) touch
 // every bank once.
 constexpr int STG_COLS = 64;
-constexpr int STG_BYTES = 32 * STG_COLS * 4;
+// Rows on no 16-byte boundary are staged plainly instead, RAGGED_LD floats to a
+// row.
+constexpr int RAGGED_LD = STG_COLS + 1;
+constexpr int STG_BYTES = 32 * RAGGED_LD * 4;
 constexpr int ACC_COLS = 256;           // tensor-memory columns per accumulator buffer
 constexpr int GN_MAX = 256;            // columns per tile
 constexpr int SPLIT_N = 128;            // columns of a tile whose contraction is shared
@@ -340,6 +343,201 @@ __device__ __forceinline__ void epilogue_rows(const GemmArgs &p, float (&v)[R][8
     else store_rows<__half, R>(q.out, step * p.ld_out, in, v);
 }
 
+// 8 elements from q on: one access where they lie on a 16-byte boundary, else
+// one each.
+template <typename T>
+__device__ __forceinline__ void load8_any(const void *q, float (&v)[8]) {
+    const T *t = static_cast<const T *>(q);
+    if ((reinterpret_cast<uintptr_t>(t) & 15) == 0) {
+        load_vec<T, 8>(t, v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = to_f(t[e]);
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store8_any(void *q, const float (&v)[8]) {
+    T *t = static_cast<T *>(q);
+    if ((reinterpret_cast<uintptr_t>(t) & 15) == 0) {
+        store_vec<T, 8>(t, v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[e] = from_f<T>(v[e]);
+    }
+}
+
+// Elements lo .. hi - 1 of a 16-byte window of a 16-bit matrix, in the largest
+// pieces that fit: the L2 takes one store per piece, and those bound rows on no
+// boundary.
+template <typename T>
+__device__ __forceinline__ void store_run(T *window, const uint32_t (&w)[4], int lo, int hi) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (lo <= 4 * h && hi >= 4 * h + 4) {
+            *reinterpret_cast<uint2 *>(window + 4 * h) = make_uint2(w[2 * h], w[2 * h + 1]);
+            continue;
+        }
+#pragma unroll
+        for (int k = 2 * h; k < 2 * h + 2; ++k) {
+            if (lo <= 2 * k && hi >= 2 * k + 2) {
+                *reinterpret_cast<uint32_t *>(window + 2 * k) = w[k];
+            } else {
+                if (lo <= 2 * k && hi > 2 * k) *reinterpret_cast<uint16_t *>(window + 2 * k) = (uint16_t)w[k];
+                if (lo <= 2 * k + 1 && hi > 2 * k + 1) *reinterpret_cast<uint16_t *>(window + 2 * k + 1) = (uint16_t)(w[k] >> 16);
+            }
+        }
+    }
+}
+// A row's first `head` and last 8 - head columns of 64: v[i] belongs into the
+// last ones' window for i < 8 - head, else into the first ones'.
+template <typename T>
+__device__ __forceinline__ void store_ends(void *row, int head, const float (&v)[8]) {
+    T *t = static_cast<T *>(row);
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
+    store_run(t + 56 + head, w, 0, 8 - head);
+    store_run(t + head - 8, w, 8 - head, 8);
+}
+
+// Epilogue of 32 rows x 64 columns whose rows start on no 16-byte boundary.  In
+// each row, pieces of 8 columns from its first boundary on take the accesses of
+// the aligned case (pre and res as well where they lie alike, as they do in
+// equal strides); then each lane finishes one row's up to 14 other elements.
+// The staged values already hold the bias, RAGGED_LD floats to a row.
+template <int ACT, int OUT>
+__device__ __forceinline__ void epilogue_ragged(const GemmArgs &p, const float *stg, int64_t row0, int col0, int lane) {
+    constexpr int R = 4;  // rows of a lane at a time
+    const int width = min(64, p.N - col0), lc = lane & 7, lr = lane >> 3;
+    if (width <= 0) return;
+    const int rows = (int)min((int64_t)32, p.M - row0);
+    // columns before the row's first 16-byte boundary
+    auto head_of = [&](int r) {
+        const uintptr_t o = reinterpret_cast<uintptr_t>(at_element(p.out, p.out_type, (row0 + r) * p.ld_out + col0));
+        return (int)((0 - o) & 15) >> (out_f32<OUT>(p) ? 2 : 1);
+    };
+    // a whole row of 16-bit results has none or 8 other elements: its last
+    // 8 - head columns and its first head ones
+    const bool ends = !out_f32<OUT>(p) && width == 64;
+    const int my_head = lane < rows ? min(head_of(lane), width) : 0;
+#pragma unroll 1
+    for (int r0 = lr; r0 < rows; r0 += 4 * R) {
+        float v[R][8], a[R][8];
+        int c[R];
+        bool in[R];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int r = r0 + 4 * k;
+            c[k] = head_of(r) + 8 * lc;
+            in[k] = r < rows && c[k] + 8 <= width;
+            if (p.res && in[k]) {
+                const char *q = at_element(p.res, p.out_type, (row0 + r) * p.ld_res + col0 + c[k]);
+                if (out_f32<OUT>(p)) load8_any<float>(q, a[k]);
+                else if (p.out_type == SC_BF16) load8_any<__nv_bfloat16>(q, a[k]);
+                else load8_any<__half>(q, a[k]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const float *s = stg + (r0 + 4 * k) * RAGGED_LD + c[k];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[k][e] = in[k] ? s[e] : 0.f;
+        }
+        if (p.pre) {
+#pragma unroll
+            for (int k = 0; k < R; ++k)
+                if (in[k]) {
+                    char *q = at_element(p.pre, p.pre_type, (row0 + r0 + 4 * k) * p.ld_pre + col0 + c[k]);
+                    if (p.pre_type == SC_F32) store8_any<float>(q, v[k]);
+                    else if (p.pre_type == SC_BF16) store8_any<__nv_bfloat16>(q, v[k]);
+                    else store8_any<__half>(q, v[k]);
+                }
+        }
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                if constexpr (ACT == SC_ACT_GELU) {
+                    const float2 g = gelu2(make_float2(v[k][e], v[k][e + 1]));
+                    v[k][e] = g.x;
+                    v[k][e + 1] = g.y;
+                } else {
+                    v[k][e] = act_fn<ACT>(v[k][e]);
+                    v[k][e + 1] = act_fn<ACT>(v[k][e + 1]);
+                }
+            }
+            if (p.res && in[k]) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[k][e] += a[k][e];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < R; ++k)
+            if (in[k]) {
+                char *o = at_element(p.out, p.out_type, (row0 + r0 + 4 * k) * p.ld_out + col0 + c[k]);
+                if (out_f32<OUT>(p)) store_vec<float, 8>(reinterpret_cast<float *>(o), v[k]);
+                else if (p.out_type == SC_BF16) store_vec<__nv_bfloat16, 8>(reinterpret_cast<__nv_bfloat16 *>(o), v[k]);
+                else store_vec<__half, 8>(reinterpret_cast<__half *>(o), v[k]);
+            }
+    }
+    if (lane < rows) {
+        const int head = my_head, tail = head + (width - head) / 8 * 8;
+        const int n = head + width - tail;
+        const int64_t row = row0 + lane;
+        if (ends) {
+            if (head == 0) return;
+            float v[8], a[8];
+            const char *res = at_element(p.res, p.out_type, row * p.ld_res + col0);
+            char *pre = at_element(p.pre, p.pre_type, row * p.ld_pre + col0);
+            char *out = at_element(p.out, p.out_type, row * p.ld_out + col0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int c = i < 8 - head ? 56 + head + i : i - 8 + head;
+                v[i] = stg[lane * RAGGED_LD + c];
+                float t[1] = {0.f};
+                if (p.res) load_any<1>(res, p.out_type, c, t);
+                a[i] = t[0];
+            }
+            if (p.pre) {
+                if (((reinterpret_cast<uintptr_t>(pre) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0 && p.pre_type != SC_F32) {
+                    if (p.pre_type == SC_BF16) store_ends<__nv_bfloat16>(pre, head, v);
+                    else store_ends<__half>(pre, head, v);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) store_any(pre, p.pre_type, i < 8 - head ? 56 + head + i : i - 8 + head, v[i]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = act_fn<ACT>(v[i]) + a[i];
+            if (p.out_type == SC_BF16) store_ends<__nv_bfloat16>(out, head, v);
+            else store_ends<__half>(out, head, v);
+            return;
+        }
+#pragma unroll 1
+        for (int i0 = 0; i0 < n; i0 += 8) {
+            float v[8], a[8];
+            int c[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int i = min(i0 + e, n - 1);  // the last one again where none is left
+                c[e] = i < head ? i : tail + i - head;
+                v[e] = stg[lane * RAGGED_LD + c[e]];
+                float t[1] = {0.f};
+                if (p.res) load_any<1>(p.res, p.out_type, row * p.ld_res + col0 + c[e], t);
+                a[e] = t[0];
+            }
+            if (p.pre) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (i0 + e < n) store_any(p.pre, p.pre_type, row * p.ld_pre + col0 + c[e], v[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (i0 + e < n) store_any(p.out, p.out_type, row * p.ld_out + col0 + c[e], act_fn<ACT>(v[e]) + a[e]);
+        }
+    }
+}
+
 // tcgen05.ld without its wait; the registers are valid after tmem_wait_ld.
 __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&v)[32]) {
     asm volatile(
@@ -438,9 +636,30 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
         const int lc = lane & 7, lr = lane >> 3;
         // 64 columns of the warp's rows: through shared memory, so that 8 lanes
         // access one row's 64 columns together
-        auto stage_quad = [&](int j, float a, float b, float c, float d) {
-            const int at = ((j & 1) * 8 + (j >> 1)) ^ (lane & 7);
-            *reinterpret_cast<float4 *>(stg + lane * STG_COLS + at * 4) = make_float4(a, b, c, d);
+        float ragged_bias[2] = {0.f, 0.f};  // of columns lane and lane + 32 of the 64 to be staged
+        auto load_ragged_bias = [&](int col0) {
+            if (p.vec || !p.bias) return;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float t[1] = {0.f};
+                if (col0 + lane + 32 * k < p.N) load_any<1>(p.bias, p.bias_type, col0 + lane + 32 * k, t);
+                ragged_bias[k] = t[0];
+            }
+        };
+        // the lane's row of 64 columns, value(i) each
+        auto stage = [&](auto value) {
+            if (p.vec) {
+#pragma unroll
+                for (int j = 0; j < STG_COLS / 4; ++j) {
+                    const int at = ((j & 1) * 8 + (j >> 1)) ^ (lane & 7);
+                    *reinterpret_cast<float4 *>(stg + lane * STG_COLS + at * 4) =
+                        make_float4(value(4 * j), value(4 * j + 1), value(4 * j + 2), value(4 * j + 3));
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < STG_COLS; ++i)
+                    stg[lane * RAGGED_LD + i] = value(i) + __shfl_sync(0xffffffffu, ragged_bias[i >> 5], i & 31);
+            }
         };
         constexpr int R = 4;  // rows of a lane at a time: lr + 4 k
         constexpr int OUT = SPLIT ? OUT_ANY : KEEP ? OUT_F32 : OUT_16;
@@ -510,18 +729,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
                     }
                 }
             } else {
-                // rows on no 16-byte boundary: one column per lane
-                for (int h = 0; h < STG_COLS; h += 32) {
-                    const int c = h + lane, j = c >> 2, col = col0 + c;
-                    if (col >= p.N) break;
-                    float b[1] = {0.f};
-                    if (p.bias) load_any<1>(p.bias, p.bias_type, col, b);
-                    const int at = (j & 1) * 8 + (j >> 1);
-                    const int rows = (int)min((int64_t)32, p.M - row0);
-#pragma unroll 4
-                    for (int r = 0; r < rows; ++r)
-                        epilogue1<ACT>(p, stg[r * STG_COLS + (at ^ (r & 7)) * 4 + (c & 3)], b[0], row0 + r, col);
-                }
+                epilogue_ragged<ACT, OUT>(p, stg, row0, col0, lane);
             }
             __syncwarp();
         };
@@ -584,9 +792,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
                         if (c >= half) break;
                         float b[8] = {};
                         load_bias(n0 + c, b);
-#pragma unroll
-                        for (int j = 0; j < STG_COLS / 4; ++j)
-                            stage_quad(j, v[c + 4 * j], v[c + 4 * j + 1], v[c + 4 * j + 2], v[c + 4 * j + 3]);
+                    load_ragged_bias(n0 + c);
+                        stage([&](int i) { return v[c + i]; });
                         store_staged(row0, n0 + c, b, c + STG_COLS < half);
                     }
                 }
@@ -598,17 +805,13 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
                 for (int c = 0; c < half; c += STG_COLS) {
                     float b[8] = {};
                     load_bias(n0 + c, b);
+                    load_ragged_bias(n0 + c);
                     uint32_t r[2][32];
                     tmem_ld32_async(lane_acc + buf * ACC_COLS + c, r[0]);
                     tmem_ld32_async(lane_acc + buf * ACC_COLS + c + 32, r[1]);
                     tmem_wait_ld(r[0]);
                     tmem_wait_ld(r[1]);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            stage_quad(k * 8 + j, __uint_as_float(r[k][4 * j]), __uint_as_float(r[k][4 * j + 1]),
-                                       __uint_as_float(r[k][4 * j + 2]), __uint_as_float(r[k][4 * j + 3]));
+                    stage([&](int i) { return __uint_as_float(r[i >> 5][i & 31]); });
                     if (c + STG_COLS >= half) release(buf);
                     store_staged(row0, n0 + c, b, c + STG_COLS < half);
                 }
@@ -731,11 +934,17 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
     } else if (warp == 3) {
         // ================= column sums =================
         if (p.sums.part) {
-            for (int64_t c = (int64_t)blockIdx.x * 32 + lane; c < p.sums.cols; c += (int64_t)gridDim.x * 32) {
+            // 8 columns at a time, a quarter of the partial rows per lane
+            for (int64_t c0 = (int64_t)blockIdx.x * 8; c0 < p.sums.cols; c0 += (int64_t)gridDim.x * 8) {
+                const int64_t c = c0 + (lane & 7);
                 float v = 0.f;
+                if (c < p.sums.cols) {
 #pragma unroll 16
-                for (int i = 0; i < p.sums.n; ++i) v += p.sums.part[i * p.sums.cols + c];
-                store_any(p.sums.out, p.sums.type, c, v);
+                    for (int i = lane >> 3; i < p.sums.n; i += 4) v += p.sums.part[i * p.sums.cols + c];
+                }
+                v += __shfl_xor_sync(0xffffffffu, v, 8);
+                v += __shfl_xor_sync(0xffffffffu, v, 16);
+                if (lane < 8 && c < p.sums.cols) store_any(p.sums.out, p.sums.type, c, v);
             }
         }
         __syncwarp();

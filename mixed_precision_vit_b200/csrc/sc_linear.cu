@@ -18,7 +18,8 @@ struct PassJob {
     const void *in, *pre;  // pre: null without an activation
     void *dst;             // null: column sums only
     float *part;           // [chunks][cols] column sums, or null
-    int vec;               // 8 columns per access
+    int vec;               // rows of 8-column pieces on 16-byte boundaries
+    int lanes;             // lanes per row (a power of two): 8 columns each
     int chunks;            // blocks that share the rows of one group of columns
     int first_block;
 };
@@ -43,77 +44,106 @@ __device__ __forceinline__ void split3(float x, __nv_bfloat16 (&p)[3]) {
     p[2] = __float2bfloat16_rn(r - __bfloat162float(p[1]));
 }
 
-// Columns of one block: 8 contiguous ones per lane, or (rows on no 16-byte
-// boundary) 4 per lane, 32 apart.
-constexpr int VEC_COLS = 256, SCALAR_COLS = 128;
+// 8 elements from p on with the widest accesses that its address allows (the
+// same for every lane of a row): 16 bytes, 4 or 2 elements, or 2 elements after
+// a first one.  n < 8: only n exist.
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, int n, float (&v)[8]) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    if (n < 8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < n ? to_f(p[i]) : 0.f;
+    } else if ((at & 15) == 0) {
+        load_vec<T, 8>(p, v);
+    } else if ((at & (4 * sizeof(T) - 1)) == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+            float t[4];
+            load_vec<T, 4>(p + i, t);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[i + k] = t[k];
+        }
+    } else if ((at & (2 * sizeof(T) - 1)) == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            float t[2];
+            load_vec<T, 2>(p + i, t);
+            v[i] = t[0];
+            v[i + 1] = t[1];
+        }
+    } else {
+        v[0] = to_f(p[0]);
+#pragma unroll
+        for (int i = 1; i < 7; i += 2) {
+            float t[2];
+            load_vec<T, 2>(p + i, t);
+            v[i] = t[0];
+            v[i + 1] = t[1];
+        }
+        v[7] = to_f(p[7]);
+    }
+}
 
-// One block's share of a job: 8 warps take a row each.  Bound by device memory.
+constexpr int BLOCK_COLS = 256;  // most columns of a block: 8 per lane
+
+// One block's share of a job: `lanes` lanes take 8 columns each of a row, so a
+// warp takes 32 / lanes rows and the block 8 times that.  The copy's rows are
+// padded with zeros to a multiple of 8 columns.  Bound by device memory.
+// VEC: all of it lies on 16-byte boundaries.
 template <typename TIN, typename T, int OUT, int ACT, bool VEC>
-__device__ __forceinline__ void run_job(const PassJob &p, int block, float (*sums)[VEC_COLS]) {
-    constexpr int E = VEC ? 8 : 4, COLS = VEC ? VEC_COLS : SCALAR_COLS;
+__device__ __forceinline__ void run_job(const PassJob &p, int block, float (*sums)[BLOCK_COLS]) {
     const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
-    const int64_t col0 = (int64_t)(block / p.chunks) * COLS;
+    const int64_t col0 = (int64_t)(block / p.chunks) * BLOCK_COLS, col = col0 + (lane & (p.lanes - 1)) * 8;
     const int chunk = block % p.chunks;
-    // column of the lane's element e
-    auto col = [&](int e) { return col0 + (VEC ? lane * 8 + e : lane + 32 * e); };
-    float s[E];
+    const int per_warp = 32 / p.lanes, per_block = 8 * per_warp;
+    const int n = (int)(p.cols - col < 8 ? p.cols - col : 8);
+    float s[8];
 #pragma unroll
-    for (int e = 0; e < E; ++e) s[e] = 0.f;
-    if (col(0) < p.cols) {
-        for (int64_t row = (int64_t)chunk * 8 + q; row < p.rows; row += (int64_t)p.chunks * 8) {
-            const TIN *in = static_cast<const TIN *>(p.in) + row * p.ld_in;
-            const T *pre = static_cast<const T *>(p.pre) + row * p.ld_pre;
-            float v[E], z[E];
-            if constexpr (VEC) {
-                load_vec<TIN, 8>(in + col(0), v);
-                if constexpr (ACT != SC_ACT_NONE) load_vec<T, 8>(pre + col(0), z);
-            } else {
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    v[e] = col(e) < p.cols ? to_f(in[col(e)]) : 0.f;
-                    if constexpr (ACT != SC_ACT_NONE) z[e] = col(e) < p.cols ? to_f(pre[col(e)]) : 0.f;
-                }
+    for (int e = 0; e < 8; ++e) s[e] = 0.f;
+    if (n > 0) {
+        for (int64_t row = (int64_t)chunk * per_block + q * per_warp + lane / p.lanes; row < p.rows;
+             row += (int64_t)p.chunks * per_block) {
+            float v[8];
+            const TIN *in = static_cast<const TIN *>(p.in) + row * p.ld_in + col;
+            if constexpr (VEC) load_vec<TIN, 8>(in, v);
+            else load8(in, n, v);
+            if constexpr (ACT != SC_ACT_NONE) {
+                const T *pre = static_cast<const T *>(p.pre) + row * p.ld_pre + col;
+                float z[8];
+                if constexpr (VEC) load_vec<T, 8>(pre, z);
+                else load8(pre, n, z);
+                times_act_grad<ACT, 8>(v, z);
             }
-            if constexpr (ACT != SC_ACT_NONE) times_act_grad<ACT, E>(v, z);
 #pragma unroll
-            for (int e = 0; e < E; ++e) s[e] += v[e];
+            for (int e = 0; e < 8; ++e) s[e] += v[e];
             if constexpr (OUT == OUT_COPY) {
-                T *d = static_cast<T *>(p.dst) + row * p.ld_dst;
-                if constexpr (VEC) {
-                    store_vec<T, 8>(d + col(0), v);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < E; ++e)
-                        if (col(e) < p.cols) d[col(e)] = from_f<T>(v[e]);
-                }
+                store_vec<T, 8>(static_cast<T *>(p.dst) + row * p.ld_dst + col, v);
             } else if constexpr (OUT == OUT_PLANES) {
-                __nv_bfloat16 *d = static_cast<__nv_bfloat16 *>(p.dst) + row * p.ld_dst;
-                float o[3][E];
+                __nv_bfloat16 *d = static_cast<__nv_bfloat16 *>(p.dst) + row * p.ld_dst + col;
+                float o[3][8];
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
+                for (int e = 0; e < 8; ++e) {
                     __nv_bfloat16 t[3];
                     split3(v[e], t);
 #pragma unroll
                     for (int k = 0; k < 3; ++k) o[k][e] = __bfloat162float(t[k]);
                 }
 #pragma unroll
-                for (int k = 0; k < 3; ++k) {
-                    if constexpr (VEC) {
-                        store_vec<__nv_bfloat16, 8>(d + k * p.plane + col(0), o[k]);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < E; ++e)
-                            if (col(e) < p.cols) d[k * p.plane + col(e)] = __float2bfloat16_rn(o[k][e]);
-                    }
-                }
+                for (int k = 0; k < 3; ++k) store_vec<__nv_bfloat16, 8>(d + k * p.plane, o[k]);
             }
         }
     }
     if (!p.part) return;
+    // the warp's rows, then the block's
+    for (int o = 16; o >= p.lanes; o >>= 1)
 #pragma unroll
-    for (int e = 0; e < E; ++e) sums[q][col(e) - col0] = s[e];
+        for (int e = 0; e < 8; ++e) s[e] += __shfl_xor_sync(0xffffffffu, s[e], o);
+    if (lane < p.lanes) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sums[q][lane * 8 + e] = s[e];
+    }
     __syncthreads();
-    if (threadIdx.x < COLS && col0 + threadIdx.x < p.cols) {
+    if ((int)threadIdx.x < p.lanes * 8 && col0 + threadIdx.x < p.cols) {
         float v = sums[0][threadIdx.x];
 #pragma unroll
         for (int k = 1; k < 8; ++k) v += sums[k][threadIdx.x];
@@ -126,7 +156,7 @@ __global__ void __launch_bounds__(256) pass_kernel(const __grid_constant__ PassA
     // the matrix product that follows may set itself up now; it waits for this
     // grid's end before it reads
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    __shared__ float sums[8][VEC_COLS];
+    __shared__ float sums[8][BLOCK_COLS];
     constexpr int OUT = sizeof(T) == 4 ? OUT_PLANES : OUT_COPY;
     int j = 0;
     while (j + 1 < p.n && (int)blockIdx.x >= p.job[j + 1].first_block) ++j;
@@ -141,15 +171,21 @@ __global__ void __launch_bounds__(256) pass_kernel(const __grid_constant__ PassA
     }
 }
 
-// Partial rows of column sums: enough blocks to fill the device, few enough for
-// one warp to add them up while a matrix product runs.
-constexpr int MAX_CHUNKS = 64;
+int pass_lanes(int64_t cols) {
+    int l = 1;
+    while (l < 32 && l * 8 < cols) l *= 2;
+    return l;
+}
 
-int pass_chunks(int64_t rows, int64_t cols, bool vec) {
+// Blocks that share a group of columns: 4 per SM in all, which run at one time
+// (fc1's gradients take 76 us so, 81 to 85 with 3, 5, 6 or 8 per SM); with column
+// sums at most 256, which one warp adds up while a product runs.
+int pass_chunks(int64_t rows, int64_t cols, bool sums) {
     if (rows < 1 || cols < 1) return 1;
-    int64_t c = div_up(8 * (int64_t)sm_count(), div_up(cols, vec ? VEC_COLS : SCALAR_COLS));
-    if (c > div_up(rows, 8)) c = div_up(rows, 8);
-    return (int)(c < MAX_CHUNKS ? c : MAX_CHUNKS);
+    const int64_t most = div_up(rows, 8 * 32 / pass_lanes(cols));
+    int64_t c = div_up(4 * (int64_t)sm_count(), div_up(cols, BLOCK_COLS));
+    if (sums && c > 256) c = 256;
+    return (int)(c < most ? c : most);
 }
 
 template <typename TIN, typename T, int OUT0>
@@ -192,9 +228,10 @@ struct Passes {
         for (int i = 0; i < a.n; ++i) {
             PassJob &j = a.job[i];
             if (blocks > INT32_MAX / 2) break;
-            j.chunks = pass_chunks(j.rows, j.cols, j.vec);
+            j.lanes = pass_lanes(j.cols);
+            j.chunks = pass_chunks(j.rows, j.cols, j.part != nullptr);
             j.first_block = (int)blocks;
-            blocks += div_up(j.cols, j.vec ? VEC_COLS : SCALAR_COLS) * j.chunks;
+            blocks += div_up(j.cols, BLOCK_COLS) * j.chunks;
         }
         if (blocks > INT32_MAX / 2) {
             set_error("sc_linear: the operands are too large");
@@ -314,7 +351,7 @@ bool dz_in_place(const sc_linear_desc &d, const void *dout) {
 }
 
 int64_t part_bytes(const sc_linear_desc &d) {
-    return round_up(MAX_CHUNKS * d.N * (int64_t)sizeof(float), 256);
+    return round_up((int64_t)pass_chunks(d.M, d.N, true) * d.N * (int64_t)sizeof(float), 256);
 }
 
 int64_t bwd_workspace(const sc_linear_desc &d, const void *dout, const void *x, const void *w) {
