@@ -400,6 +400,29 @@ __device__ __forceinline__ void store_ends(void *row, int head, const float (&v)
     store_run(t + head - 8, w, 8 - head, 8);
 }
 
+// The same columns' values, in the order of store_ends, by one access for each
+// window that lies in the row: from column -8 on if `before`, up to column 71 if
+// `after`; else one by one.  Elements outside the 64 columns are not used.
+template <typename T>
+__device__ __forceinline__ void load_ends(const void *row, int head, bool before, bool after, float (&v)[8]) {
+    const T *t = static_cast<const T *>(row);
+    float a[8], b[8];
+    if (after) {
+        load_vec<T, 8>(t + 56 + head, a);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a[i] = i < 8 - head ? to_f(t[56 + head + i]) : 0.f;
+    }
+    if (before) {
+        load_vec<T, 8>(t + head - 8, b);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) b[i] = i >= 8 - head ? to_f(t[i - 8 + head]) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < 8 - head ? a[i] : b[i];
+}
+
 // Epilogue of 32 rows x 64 columns whose rows start on no 16-byte boundary.  In
 // each row, pieces of 8 columns from its first boundary on take the accesses of
 // the aligned case (pre and res as well where they lie alike, as they do in
@@ -490,14 +513,20 @@ __device__ __forceinline__ void epilogue_ragged(const GemmArgs &p, const float *
             const char *res = at_element(p.res, p.out_type, row * p.ld_res + col0);
             char *pre = at_element(p.pre, p.pre_type, row * p.ld_pre + col0);
             char *out = at_element(p.out, p.out_type, row * p.ld_out + col0);
+            if (p.res && ((reinterpret_cast<uintptr_t>(res) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0) {
+                const bool before = col0 > 0, after = col0 + 64 + head <= p.N;
+                if (p.out_type == SC_BF16) load_ends<__nv_bfloat16>(res, head, before, after, a);
+                else load_ends<__half>(res, head, before, after, a);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int c = i < 8 - head ? 56 + head + i : i - 8 + head;
-                v[i] = stg[lane * RAGGED_LD + c];
-                float t[1] = {0.f};
-                if (p.res) load_any<1>(res, p.out_type, c, t);
-                a[i] = t[0];
+                for (int i = 0; i < 8; ++i) {
+                    float t[1] = {0.f};
+                    if (p.res) load_any<1>(res, p.out_type, i < 8 - head ? 56 + head + i : i - 8 + head, t);
+                    a[i] = t[0];
+                }
             }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = stg[lane * RAGGED_LD + (i < 8 - head ? 56 + head + i : i - 8 + head)];
             if (p.pre) {
                 if (((reinterpret_cast<uintptr_t>(pre) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0 && p.pre_type != SC_F32) {
                     if (p.pre_type == SC_BF16) store_ends<__nv_bfloat16>(pre, head, v);

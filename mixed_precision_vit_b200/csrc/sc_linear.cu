@@ -177,13 +177,14 @@ int pass_lanes(int64_t cols) {
     return l;
 }
 
-// Blocks that share a group of columns: 4 per SM in all, which run at one time
-// (fc1's gradients take 76 us so, 81 to 85 with 3, 5, 6 or 8 per SM); with column
-// sums at most 256, which one warp adds up while a product runs.
+// Blocks that share a group of columns: 8 per SM in all for copies; with column
+// sums 4 per SM, which run at one time (fc1's gradients take 76 us so, 81 to 85
+// with 3, 5, 6 or 8), and at most 256, which one warp adds up while a product
+// runs.
 int pass_chunks(int64_t rows, int64_t cols, bool sums) {
     if (rows < 1 || cols < 1) return 1;
     const int64_t most = div_up(rows, 8 * 32 / pass_lanes(cols));
-    int64_t c = div_up(4 * (int64_t)sm_count(), div_up(cols, BLOCK_COLS));
+    int64_t c = div_up((sums ? 4 : 8) * (int64_t)sm_count(), div_up(cols, BLOCK_COLS));
     if (sums && c > 256) c = 256;
     return (int)(c < most ? c : most);
 }
