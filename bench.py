@@ -80,18 +80,33 @@ CONFIG_TEXT = {
 }
 
 
+# the floating-point layers: kernels of their own, which no workload here runs
+LAYER_SOURCES = ("sc_gemm", "sc_layers", "sc_linear", "sc_norm")
+LAYER_SECTION = ("/* ---- floating-point layers of a transformer block",
+                 "/* ---- end of the floating-point layers --------------------------------------- */\n\n")
+
+
 def kernel_source_hash() -> str:
     """First 12 hex digits of the SHA-256 of the library's CUDA sources
-    (csrc/*.cu, *.cuh, include/sc.h), in name order."""
+    (csrc/*.cu, *.cuh, include/sc.h), in name order, without the floating-point
+    layers' files and their section of the header."""
     import glob
     import hashlib
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "mixed_precision_vit_b200", "csrc")
     for p in sorted(glob.glob(os.path.join(csrc, "*.cu")) + glob.glob(os.path.join(csrc, "*.cuh"))
                     + [os.path.join(ROOT, "include", "sc.h")]):
-        h.update(os.path.basename(p).encode())
+        name = os.path.basename(p)
+        if name.startswith(LAYER_SOURCES):
+            continue
         with open(p, "rb") as f:
-            h.update(f.read())
+            data = f.read()
+        if name == "sc.h":
+            begin, end = (m.encode() for m in LAYER_SECTION)
+            if begin in data and end in data:
+                data = data[:data.index(begin)] + data[data.index(end) + len(end):]
+        h.update(name.encode())
+        h.update(data)
     return h.hexdigest()[:12]
 
 

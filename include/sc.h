@@ -452,7 +452,9 @@ int sc_matmul_launches(const sc_matmul_desc *desc, const sc_table *table);
  * schedule leaves in floating point ("scmp_vit" README, the skip_worst
  * schedules), each with its backward pass.  The conventions at the top of this
  * file hold; matrices are row-major with a row stride ("ld", in elements) and
- * only the [rows x cols] part of a matrix is written, never its padding. */
+ * only the [rows x cols] part of a matrix is written, never its padding.
+ * Outputs overlap nothing else unless it says so below.  Pointers are aligned
+ * for their element type; rows on 16-byte boundaries are fastest. */
 
 /* element types */
 #define SC_F32 0
@@ -552,7 +554,9 @@ typedef struct sc_linear_desc {
  * Products of 16-bit operands are exact and summed in fp32 on the tensor cores;
  * fp32 operands are split into three bf16 parts each (exactly: 3 x 8 bits of
  * significand) whose six leading products are summed in fp32.  bias, act and
- * residual are applied in fp32 and out is rounded once.
+ * residual are applied in fp32 and out is rounded once.  The tensor cores cut
+ * sums where fp32 arithmetic rounds; where out is SC_F32, sums of at most 1024
+ * products are added up in fp32 arithmetic, so that long ones do not drift.
  *   bias       (device, nullable) [N]
  *   residual   (device, nullable) [M][N] of out_type
  *   out        (device) out; may be residual itself (same stride)
@@ -586,6 +590,8 @@ int sc_linear_backward(const sc_linear_desc *desc, const void *dout, const void 
 int64_t sc_linear_workspace_bytes(const sc_linear_desc *desc, const void *x, const void *w);
 int64_t sc_linear_backward_workspace_bytes(const sc_linear_desc *desc, const void *dout,
                                            const void *x, const void *w);
+
+/* ---- end of the floating-point layers --------------------------------------- */
 
 #ifdef __cplusplus
 }
