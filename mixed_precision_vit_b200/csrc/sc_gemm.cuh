@@ -106,11 +106,19 @@ __device__ __forceinline__ float2 normal2(float2 z, float2 z2) {
 // gelu(z) = z Phi(z), off by at most 4 * 2^-24 |z|.
 __device__ __forceinline__ float2 gelu2(float2 z) { return mul2(z, normal2(z, mul2(z, z))); }
 
+// 2^x, off by 2^-22 of itself (ex2.approx), 0 far below the normal range.
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // gelu'(z) = Phi(z) + z exp(-z^2 / 2) / sqrt(2 pi); the second term is 0 from
 // |z| = 16 on, which keeps infinity * 0 out.
 __device__ __forceinline__ float2 gelu_grad2(float2 z) {
     const float2 z2 = mul2(z, z);
-    const float2 e = make_float2(__expf(-0.5f * z2.x), __expf(-0.5f * z2.y));
+    const float2 a = mul2(z2, make_float2(-0.72134752f, -0.72134752f));  // -log2(e) / 2
+    const float2 e = make_float2(exp2_approx(a.x), exp2_approx(a.y));
     const float2 c = make_float2(fminf(fmaxf(z.x, -16.f), 16.f), fminf(fmaxf(z.y, -16.f), 16.f));
     return fma2(mul2(c, make_float2(0.39894228f, 0.39894228f)), e, normal2(z, z2));
 }

@@ -1,6 +1,6 @@
-// sc_gemm_dev.cuh -- the kernels of sc_gemm.cu: D(m, n) = sum_k A(m, k) B(n, k) on the 5th-generation tensor
-// cores (tcgen05.mma.kind::f16, fp32 accumulators in tensor memory), with the
-// linear layer's epilogue.
+// sc_gemm_dev.cuh -- the kernels of sc_gemm.cu: D(m, n) = sum_k A(m, k) B(n, k)
+// on the 5th-generation tensor cores (tcgen05.mma.kind::f16, fp32 accumulators in
+// tensor memory), with the linear layer's epilogue.
 //
 // Operand tiles of 64 contraction indexes (128 bytes, 128-byte swizzle) come
 // by TMA into a ring of shared-memory stages; rows and columns past the
@@ -16,17 +16,25 @@
 // The tensor cores cut an fp32 sum where fp32 arithmetic rounds, so a long sum
 // drifts towards zero by about 2^-25 of itself per 16 indexes.  Where the
 // result keeps fp32, an accumulator therefore takes CHUNK stages at most, and
-// the epilogue warps add the chunks in registers.
+// the epilogue warps add the chunks in registers (32896 x 1024 x 4096: off by
+// 9.2e-7 of the result's norm, 4.0e-6 in one accumulation).
 //
-// Kernels:
-//   gemm_kernel<2>  clusters of two CTAs on two SMs, one cta_group::2 MMA of
-//                   256 rows x bn columns; persistent over the tiles, two
-//                   accumulators, so a tile's epilogue runs under the next
-//                   tile's products
-//   gemm_kernel<1>  the same with one CTA and 128 rows
-//   gemm_split_kernel  few tiles: a cluster of CTAs shares one tile's
-//                   contraction and adds the parts over distributed shared
-//                   memory, in rank order
+// Kernels (one template):
+//   CG = 2  clusters of two CTAs on two SMs, one cta_group::2 MMA of 256 rows x
+//           256 columns, so that each SM stages half of the columns' operand;
+//           persistent over the tiles, two accumulators, so that a tile's
+//           epilogue runs under the next tile's products
+//   CG = 1  the same with one CTA and 128 rows x 128 columns
+//   SPLIT   few tiles: a cluster of CTAs shares one tile's contraction and adds
+//           the parts over distributed shared memory, in rank order
+// Warp 0 issues the copies, warp 1 the products, warp 3 finishes column sums of
+// an earlier pass if the caller has any, warps 4 to 11 are the epilogue.
+//
+// Measured (us, one B200, inputs larger than L2 in turn): 8192^3 bf16 692
+// (cuBLAS 689); 4112 x 4096 x 1024 26 plain (cuBLAS 27), 36 with gelu and the
+// pre-activation kept, where the epilogue sets the pace (tensor pipe 55 % busy);
+// 32896 x 1024 x 4096 with an fp32 residual and result 216 (tensor pipe 79 %;
+// cuBLAS 195 without either).
 // All waits are bounded, as in the count engine: on expiry the kernel records
 // SC_DEV_WAIT_LIMIT, waits for its own copies and products, frees tensor
 // memory and returns.
@@ -59,7 +67,7 @@ constexpr int STG_COLS = 64;
 constexpr int RAGGED_LD = STG_COLS + 1;
 constexpr int STG_BYTES = 32 * RAGGED_LD * 4;
 constexpr int ACC_COLS = 256;           // tensor-memory columns per accumulator buffer
-constexpr int GN_MAX = 256;            // columns per tile
+constexpr int GN_MAX = 256;             // columns per tile
 constexpr int SPLIT_N = 128;            // columns of a tile whose contraction is shared
 constexpr int SPLIT_LD = SPLIT_N + 4;
 constexpr int MAX_PARTS = 8;            // the portable cluster size
@@ -967,9 +975,15 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
             for (int64_t c0 = (int64_t)blockIdx.x * 8; c0 < p.sums.cols; c0 += (int64_t)gridDim.x * 8) {
                 const int64_t c = c0 + (lane & 7);
                 float v = 0.f;
-                if (c < p.sums.cols) {
-#pragma unroll 16
-                    for (int i = lane >> 3; i < p.sums.n; i += 4) v += p.sums.part[i * p.sums.cols + c];
+                for (int i0 = lane >> 3; i0 < p.sums.n; i0 += 32) {
+                    float t[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int i = i0 + 4 * k;
+                        t[k] = i < p.sums.n && c < p.sums.cols ? p.sums.part[i * p.sums.cols + c] : 0.f;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v += t[k];
                 }
                 v += __shfl_xor_sync(0xffffffffu, v, 8);
                 v += __shfl_xor_sync(0xffffffffu, v, 16);

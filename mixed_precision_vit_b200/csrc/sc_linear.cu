@@ -88,7 +88,9 @@ constexpr int BLOCK_COLS = 256;  // most columns of a block: 8 per lane
 
 // One block's share of a job: `lanes` lanes take 8 columns each of a row, so a
 // warp takes 32 / lanes rows and the block 8 times that.  The copy's rows are
-// padded with zeros to a multiple of 8 columns.  Bound by device memory.
+// padded with zeros to a multiple of 8 columns.  Copies are bound by device
+// memory; dz of a gelu layer by its instructions (4112 x 4096 bf16: 28 us from
+// device memory, 16 at the copy's rate; schedulers 56 % busy).
 // VEC: all of it lies on 16-byte boundaries.
 template <typename TIN, typename T, int OUT, int ACT, bool VEC>
 __device__ __forceinline__ void run_job(const PassJob &p, int block, float (*sums)[BLOCK_COLS]) {
@@ -115,7 +117,11 @@ __device__ __forceinline__ void run_job(const PassJob &p, int block, float (*sum
                 times_act_grad<ACT, 8>(v, z);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s[e] += v[e];
+            for (int e = 0; e < 8; e += 2) {
+                const float2 t = add2(make_float2(s[e], s[e + 1]), make_float2(v[e], v[e + 1]));
+                s[e] = t.x;
+                s[e + 1] = t.y;
+            }
             if constexpr (OUT == OUT_COPY) {
                 store_vec<T, 8>(static_cast<T *>(p.dst) + row * p.ld_dst + col, v);
             } else if constexpr (OUT == OUT_PLANES) {
@@ -177,14 +183,13 @@ int pass_lanes(int64_t cols) {
     return l;
 }
 
-// Blocks that share a group of columns: 8 per SM in all for copies; with column
-// sums 4 per SM, which run at one time (fc1's gradients take 76 us so, 81 to 85
-// with 3, 5, 6 or 8), and at most 256, which one warp adds up while a product
-// runs.
+// Blocks that share a group of columns: 8 per SM in all (4 to 8 measure alike
+// for dz, fewer are slower for copies), with column sums at most 256, which one
+// warp adds up while a product runs.
 int pass_chunks(int64_t rows, int64_t cols, bool sums) {
     if (rows < 1 || cols < 1) return 1;
     const int64_t most = div_up(rows, 8 * 32 / pass_lanes(cols));
-    int64_t c = div_up((sums ? 4 : 8) * (int64_t)sm_count(), div_up(cols, BLOCK_COLS));
+    int64_t c = div_up(8 * (int64_t)sm_count(), div_up(cols, BLOCK_COLS));
     if (sums && c > 256) c = 256;
     return (int)(c < most ? c : most);
 }
