@@ -75,6 +75,22 @@ int launch(GemmFn kern, const GemmArgs &p, int grid, int cluster, bool early, cu
     return e == cudaSuccess ? SC_OK : cuda_fail(e, "matrix product");
 }
 
+// A kernel that moves registers between its warps waits for ever if it was
+// launched with fewer than the moves add up to, so a build that gave it another
+// number is refused (asked once per kernel).
+bool keep_regs_ok(GemmFn kern) {
+    static std::atomic<GemmFn> known[16];
+    for (auto &k : known)
+        if (k.load(std::memory_order_relaxed) == kern) return true;
+    cudaFuncAttributes a;
+    if (cudaFuncGetAttributes(&a, kern) != cudaSuccess || a.numRegs != KEEP_REGS) return false;
+    for (auto &k : known) {
+        GemmFn none = nullptr;
+        if (k.compare_exchange_strong(none, kern)) break;
+    }
+    return true;
+}
+
 // Clusters of `parts` CTAs of the split kernel that fit the device at one
 // time (asked once per device and size; fewer than SMs / parts, since a
 // cluster stays within one GPC).
@@ -200,9 +216,14 @@ int launch_gemm(int64_t M, int64_t N, int64_t K, int type16, const GemmOperand &
         default: k = gemm_kernels_none(); break;
     }
     if (sh.parts > 1) return launch(k.split, p, p.n_tiles * sh.parts, sh.parts, early, stream);
-    const int units = sm_count() / sh.cg;
-    return launch((sh.cg == 2 ? k.pair : k.single)[epi.out_type == SC_F32], p,
-                  sh.cg * (p.n_tiles < units ? p.n_tiles : units), sh.cg, early, stream);
+    const int units = sm_count() / sh.cg, keep = epi.out_type == SC_F32;
+    const GemmFn kern = (sh.cg == 2 ? k.pair : k.single)[keep];
+    if (keep && !keep_regs_ok(kern)) {
+        cudaGetLastError();
+        set_error("matrix product: the kernel was built with another number of registers than %d", KEEP_REGS);
+        return SC_ERR_CUDA;
+    }
+    return launch(kern, p, sh.cg * (p.n_tiles < units ? p.n_tiles : units), sh.cg, early, stream);
 }
 
 }  // namespace scb

@@ -55,6 +55,7 @@ constexpr int A_STAGE = GM * GK * 2;    // 16 KB
 constexpr int EPI_WARPS = 8;            // two per quadrant of tensor-memory lanes
 constexpr int EPI_WARP0 = 4;
 constexpr int GEMM_THREADS = (EPI_WARP0 + EPI_WARPS) * 32;
+constexpr int KEEP_REGS = 168;          // registers per thread of a kernel that keeps sums
 constexpr int RING_BYTES = 160 * 1024;  // 5 stages of 32 KB
 constexpr int MAX_RING = 8;
 constexpr int CHUNK = 16;               // stages (1024 indexes) per accumulation of an fp32 result
@@ -616,7 +617,8 @@ __device__ __forceinline__ void tmem_free(uint32_t base) {
 }
 
 // CG CTAs per tile of CG * 128 rows.  SPLIT (CG = 1): the CTAs of a cluster
-// each take a share of one tile's contraction.  KEEP: accumulations of p.chunk stages added in registers.
+// each take a share of one tile's contraction.  KEEP: the epilogue adds up
+// accumulations of p.chunk stages in registers (fp32 results, and parts).
 template <int CG, bool SPLIT, bool KEEP, int ACT>
 __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_constant__ GemmArgs p) {
     static_assert(CG == 1 || !SPLIT, "a shared contraction has one CTA per part");
@@ -829,7 +831,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
                         if (c >= half) break;
                         float b[8] = {};
                         load_bias(n0 + c, b);
-                    load_ragged_bias(n0 + c);
+                        load_ragged_bias(n0 + c);
                         stage([&](int i) { return v[c + i]; });
                         store_staged(row0, n0 + c, b, c + STG_COLS < half);
                     }
@@ -867,8 +869,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
         if (threadIdx.x == 0 && sy.abort_flag && p.dev_status) atomicOr(p.dev_status, SC_DEV_WAIT_LIMIT);
     };
     // 128 sums per epilogue thread: those warps take registers over from the
-    // other four (launched with 168 each: 56 + 2 x 224 = 3 x 168).  The two
-    // sides share no code after this.
+    // other four (launched with KEEP_REGS each, which the host checks: 56 + 2 x
+    // 224 = 3 x 168).  The two sides share no code after this.
     if constexpr (KEEP && !SPLIT) {
         if (warp >= EPI_WARP0) {
             asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
@@ -963,7 +965,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
             }
             if (*abort_flag) {  // gave up: let the products that were issued finish
                 int dummy = 0;
-                if (elect_one()) mma_commit<1>(&sy.drain);
+                if (elect_one()) mma_commit<CG>(&sy.drain);
                 mbar_wait(&sy.drain, 0, &dummy, WAIT_LIMIT_CYCLES / 16);
             }
         }

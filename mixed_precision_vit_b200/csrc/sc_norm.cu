@@ -51,8 +51,7 @@ __device__ __forceinline__ float row_sum(float v, float *red) {
 }
 
 // T threads per row, each holding NC chunks of E columns (chunk c of thread t
-// starts at column (c T + t) E), so D <= T NC E.  VEC: every chunk is inside
-// the row and aligned; otherwise E = 1.
+// starts at column (c T + t) E), so D <= T NC E; rows and D are aligned for E.
 template <typename TX, typename TY, int E, int NC, int T>
 __global__ void __launch_bounds__(T < 128 ? 128 : T) ln_fwd_kernel(const NormArgs p) {
     constexpr int RPB = T < 128 ? 128 / T : 1;

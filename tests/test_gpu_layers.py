@@ -395,6 +395,33 @@ def test_linear_activations(act, t):
         check_linear(x, w, bias, None, act, F32, want_pre=True)
 
 
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("M,N,K,t,ot", [(4112, 1600, 1100, BF16, F32), (4112, 1601, 200, F16, F16),
+                                        (4112, 1603, 1100, F16, F32), (1300, 1290, 90, BF16, BF16)])
+def test_linear_activations_of_many_tiles(M, N, K, t, ot, act):
+    g = gen(15)
+    x, w = rnd(g, M, K, dtype=t), rnd(g, N, K, dtype=t, scale=2 * K ** -0.5)
+    check_linear(x, w, rnd(g, N), rnd(g, M, N, dtype=ot), act, ot, want_pre=True)
+
+
+@pytest.mark.parametrize("t,ot", [(BF16, BF16), (F16, F32)])
+def test_linear_rows_on_different_boundaries(t, ot):
+    """Results, residuals and pre-activations whose rows begin on other boundaries than each
+    other's, and a residual that is the result."""
+    g = gen(16)
+    M, N, K = 700, 333, 96
+    x, w = rnd(g, M, K, dtype=t), rnd(g, N, K, dtype=t, scale=0.1)
+    b = rnd(g, N + 1, dtype=t)[1:]
+    for po, pr in ((0, 0), (1, 0), (3, 8), (19, 2)):
+        res, _ = strided(rnd(g, M, N, dtype=ot), pr)
+        out, big = strided(torch.zeros(M, N, dtype=ot, device="cuda"), po)
+        a, _ = check_linear(x, w, b, res, "gelu", ot, want_pre=True, out=out)
+        assert big[:, N:].isnan().all()
+        keep, _ = strided(res, po)
+        sc.linear(x, w, b, keep, "gelu", out_dtype=ot, out=keep)
+        assert torch.equal(keep, a)
+
+
 @pytest.mark.parametrize("t", [BF16, F32])
 @pytest.mark.parametrize("pad", [1, 8])
 def test_linear_strided_and_untouched_padding(t, pad):
