@@ -133,25 +133,36 @@ struct Shape {
 // 0.005 per column and part.  So 4112 x 1024 x 4096 takes 25.5 in pairs
 // (68 tiles, one round) and 37.2 in single CTAs (264 tiles, two rounds); 2056 x
 // 1024 x 1024 takes 10.6 and 8.5; 257 x 1024 x 4096 takes 13.0 in 4 parts of
-// 128 columns and 28 unshared.
-Shape choose(int64_t M, int64_t N, int n_it) {
+// 128 columns and 28 unshared.  A step of fp32 operands (three stages, six
+// products) costs 1.75 in a pair, 1.2 in a CTA alone, 1.1 and 1.0 in parts of 128
+// and 64 columns: 257 x 1024 x 1024 takes 17.2 in 4 parts of 128, 18.2 in 2 of 64,
+// 28.4 unshared, all with their operands' pass; 4112 x 1024 x 1024 49.2 in pairs
+// and 56.4 in single CTAs.
+Shape choose(int64_t M, int64_t N, int n_k, int planes) {
     const int sms = sm_count();
     auto rounds = [](int64_t tiles, int units) { return (double)div_up(tiles, units < 1 ? 1 : units); };
     const int64_t rows = div_up(M, GM);
+    const bool f32 = planes == 3;
     Shape best = {2, 256, 1};
-    double least = 6.0 + 0.30 * n_it * rounds(div_up(M, 2 * GM) * div_up(N, 256), sms / 2);
+    double least = 6.0 + (f32 ? 1.75 : 0.30) * n_k * rounds(div_up(M, 2 * GM) * div_up(N, 256), sms / 2);
     auto consider = [&](const Shape &s, double t) {
         if (t < least) {
             least = t;
             best = s;
         }
     };
-    consider({1, 128, 1}, 5.0 + 0.24 * n_it * rounds(rows * div_up(N, 128), sms));
+    consider({1, 128, 1}, 5.0 + (f32 ? 1.2 : 0.24) * n_k * rounds(rows * div_up(N, 128), sms));
     for (int bn = 64; bn <= SPLIT_N; bn *= 2) {
         const int64_t tiles = rows * div_up(N, bn);
-        for (int parts = 2; parts <= MAX_PARTS && 2 * parts <= n_it && tiles * parts <= sms; ++parts)
-            if (tiles <= split_clusters(parts))
-                consider({1, bn, parts}, 5.0 + 0.008 * bn + 0.005 * bn * parts + 0.24 * (double)div_up(n_it, parts));
+        const double step = !f32 ? 0.24 : bn == 64 ? 1.0 : 1.1;
+        // each part of a shared tile takes two stages or more
+        for (int parts = 2; parts <= MAX_PARTS && 2 * parts <= planes * n_k && parts <= n_k && tiles * parts <= sms;
+             ++parts)
+            // One cluster fewer than fit: a device full of them does not pay
+            // (257 x 1024 x 1024 fp32 in 24 clusters of 5 CTAs, all that fit:
+            // 19.0, of 4 17.2; 16-bit operands alike in both).
+            if (tiles < split_clusters(parts))
+                consider({1, bn, parts}, 5.0 + 0.008 * bn + 0.005 * bn * parts + step * (double)div_up(n_k, parts));
     }
     return best;
 }
@@ -162,10 +173,13 @@ int launch_gemm(int64_t M, int64_t N, int64_t K, int type16, const GemmOperand &
                 const GemmEpilogue &epi, GemmAfter after, const ColumnSums *sums, int32_t *dev_status,
                 cudaStream_t stream) {
     GemmArgs p;
-    p.n_prod = a.planes == 3 ? 6 : 1;
+    p.planes = a.planes;
     p.n_k = (int)div_up(K, GK);
-    const Shape sh = choose(M, N, p.n_k * p.n_prod);
-    p.chunk = epi.out_type == SC_F32 || sh.parts > 1 ? CHUNK : p.n_k * p.n_prod;
+    const Shape sh = choose(M, N, p.n_k, p.planes);
+    p.chunk = epi.out_type != SC_F32 && sh.parts == 1 ? p.n_k : p.planes == 1 ? CHUNK : CHUNK_F32;
+    // the two accumulators of fp32 operands: twice where two tiles' fit
+    p.rest = p.planes == 1 ? 0 : sh.bn <= ACC_COLS / 2 ? ACC_COLS / 2 : ACC_COLS;
+    p.acc_two = p.rest < ACC_COLS;
     p.bn = sh.bn;
     p.M = (int)M;
     p.N = (int)N;

@@ -10,14 +10,23 @@
 //
 // fp32 operands: x = x1 + x2 + x3 exactly, bf16 parts of 8 bits of
 // significand, |x2| <= 2^-8 |x|, |x3| <= 2^-16 |x|.  Of the nine products the
-// three below 2^-24 |x w| are left out; the others run as six products over
-// the planes, the small ones first.
+// three below 2^-24 |x w| are left out.  The same part of both operands makes a
+// stage, and the other six products run as their stages arrive, so that 64
+// indexes take three stages.  (257 x 1024 x 1024 with its pass takes 17.3 us, 2056
+// x 1024 x 1024 32; as six products over the parts one after the other, 19.4 and
+// 38; with the six operand tiles as stages of their own 21.7 and 38: every stage
+// costs the issuing threads its waits.)
 //
 // The tensor cores cut an fp32 sum where fp32 arithmetic rounds, so a long sum
 // drifts towards zero by about 2^-25 of itself per 16 indexes.  Where the
-// result keeps fp32, an accumulator therefore takes CHUNK stages at most, and
+// result keeps fp32, an accumulator therefore takes CHUNK steps at most, and
 // the epilogue warps add the chunks in registers (32896 x 1024 x 4096: off by
-// 9.2e-7 of the result's norm, 4.0e-6 in one accumulation).
+// 9.2e-7 of the result's norm, 4.0e-6 in one accumulation; CHUNK / 2 would make
+// it 4.7e-7 in 243 us instead of 230).  fp32 operands keep the five small
+// products, below 2^-8 of the result, in an accumulator of their own, so that
+// only the leading product's drift counts, and take CHUNK_F32 steps (8: off by
+// 4.7e-7 where 16 are off by 1.0e-6; 4112 x 4096 x 1024 takes 164 us, 160 with
+// 16; a plain fp32 product is off by 5.7e-7).
 //
 // Kernels (one template):
 //   CG = 2  clusters of two CTAs on two SMs, one cta_group::2 MMA of 256 rows x
@@ -58,7 +67,8 @@ constexpr int GEMM_THREADS = (EPI_WARP0 + EPI_WARPS) * 32;
 constexpr int KEEP_REGS = 168;          // registers per thread of a kernel that keeps sums
 constexpr int RING_BYTES = 160 * 1024;  // 5 stages of 32 KB
 constexpr int MAX_RING = 8;
-constexpr int CHUNK = 16;               // stages (1024 indexes) per accumulation of an fp32 result
+constexpr int CHUNK = 16;               // steps (1024 indexes) per accumulation of an fp32 result
+constexpr int CHUNK_F32 = 8;            // with fp32 operands
 // Epilogue staging, per warp: 32 rows x 64 columns of fp32, 16-byte quads
 // permuted so that both a lane's row (written) and 8 lanes' row (read) touch
 // every bank once.
@@ -81,9 +91,11 @@ struct GemmArgs {
     void *out, *pre;
     int32_t *dev_status;
     int M, N;
-    int n_k;            // stages of one product
-    int n_prod;         // 1, or 6 for fp32 operands
-    int chunk;          // stages per accumulation
+    int n_k;            // steps of 64 contraction indexes
+    int planes;         // stages per step: 1, or 3 for fp32 operands
+    int chunk;          // steps per accumulation
+    int acc_two;        // 1: two accumulations fit tensor memory, 0: one
+    int rest;           // columns from the leading parts' accumulator to the others', fp32 operands
     int a_mn, b_mn;     // operand has its own index contiguous
     int bn;             // columns per tile
     int n_tiles_m, n_tiles_n, n_tiles;
@@ -106,10 +118,6 @@ struct GemmSync {
 constexpr int GEMM_SMEM = RING_BYTES + EPI_WARPS * STG_BYTES + 1024 + 512;
 static_assert(sizeof(GemmSync) <= 512, "barriers");
 static_assert(GEMM_SMEM <= 227 * 1024, "shared memory");
-
-// The parts of fp32 operands that product `i` multiplies, small ones first.
-__device__ __forceinline__ int plane_a(int i, int n) { return n == 1 ? 0 : (0x001102 >> (4 * i)) & 15; }
-__device__ __forceinline__ int plane_b(int i, int n) { return n == 1 ? 0 : (0x010120 >> (4 * i)) & 15; }
 
 // A slot of the ring of stages and the parity of its current use.
 struct Ring {
@@ -208,14 +216,15 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap *map, 
     }
 }
 
-// Products of one stage: 4 MMAs of 16 contraction indexes.  da, db: the
-// descriptors of a stage at address 0; ka, kb: their steps.
+// Products of A of the stage at sa and B of the stage at sb: 4 MMAs of 16
+// contraction indexes.  da, db: the descriptors of a stage at address 0; ka, kb:
+// their steps.
 template <int CG>
 __device__ __forceinline__ void stage_mmas(uint32_t d, uint64_t da, uint64_t db, uint32_t ka, uint32_t kb,
-                                           uint32_t idesc, uint32_t sa, bool first) {
-    sa &= 0x3FFFFu;  // the offset alone: in a cluster the address also holds the CTA's rank
-    da += sa >> 4;
-    db += (sa + A_STAGE) >> 4;
+                                           uint32_t idesc, uint32_t sa, uint32_t sb, bool first) {
+    // the offsets alone: in a cluster the addresses also hold the CTA's rank
+    da += (sa & 0x3FFFFu) >> 4;
+    db += ((sb + A_STAGE) & 0x3FFFFu) >> 4;
 #pragma unroll
     for (int k = 0; k < GK / 16; ++k) mma_f16_ss<CG>(d, da + k * ka, db + k * kb, idesc, !(first && k == 0));
 }
@@ -588,6 +597,14 @@ __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&v)[32
           "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
         : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+        : "r"(taddr)
+        : "memory");
+}
 __device__ __forceinline__ void tmem_wait_ld(uint32_t (&v)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
@@ -632,13 +649,12 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
     const int rank = CG == 2 || SPLIT ? (int)cluster_rank() : 0;
     const int first_tile = CG == 2 || SPLIT ? (int)cluster_id() : (int)blockIdx.x;
     const int tile_step = SPLIT ? p.n_tiles : CG == 2 ? (int)cluster_count() : (int)gridDim.x;
-    // this CTA's share of the stages of a tile
-    const int n_it = p.n_k * p.n_prod;
-    int it0 = 0, it1 = n_it;
+    // this CTA's share of the steps of a tile
+    int it0 = 0, it1 = p.n_k;
     if constexpr (SPLIT) {
         const int parts = (int)gridDim.x / p.n_tiles;
-        it0 = (int)((int64_t)n_it * rank / parts);
-        it1 = (int)((int64_t)n_it * (rank + 1) / parts);
+        it0 = (int)((int64_t)p.n_k * rank / parts);
+        it1 = (int)((int64_t)p.n_k * (rank + 1) / parts);
     }
 
     if (threadIdx.x == 0) {
@@ -805,17 +821,21 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
                 constexpr int COLS = SPLIT ? SPLIT_N / 2 : GN_MAX / 2;
                 float v[COLS] = {};
                 for (int i = it0; i < it1; i += p.chunk, ++n) {
-                    const int buf = n & 1;
-                    if (!wait_warp(&sy.acc_full[buf], (n >> 1) & 1, abort_flag)) return;
+                    const int buf = n & p.acc_two;
+                    if (!wait_warp(&sy.acc_full[buf], (n >> p.acc_two) & 1, abort_flag)) return;
                     tc_fence_after();
+                    uint32_t acc = lane_acc + buf * ACC_COLS + p.rest;
+                    for (int left = p.rest;; left = 0, acc -= p.rest) {  // the rest first
 #pragma unroll
-                    for (int c = 0; c < COLS; c += 32) {
-                        if (c < half) {
-                            uint32_t r[32];
-                            tmem_ld32(lane_acc + buf * ACC_COLS + c, r);
+                        for (int c = 0; c < COLS; c += 32) {
+                            if (c < half) {
+                                uint32_t r[32];
+                                tmem_ld32(acc + c, r);
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) v[c + j] += __uint_as_float(r[j]);
+                                for (int j = 0; j < 32; ++j) v[c + j] += __uint_as_float(r[j]);
+                            }
                         }
+                        if (!left) break;
                     }
                     release(buf);
                 }
@@ -837,8 +857,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
                     }
                 }
             } else {
-                const int buf = n & 1;
-                if (!wait_warp(&sy.acc_full[buf], (n >> 1) & 1, abort_flag)) return;
+                const int buf = n & p.acc_two;
+                if (!wait_warp(&sy.acc_full[buf], (n >> p.acc_two) & 1, abort_flag)) return;
                 ++n;
                 tc_fence_after();
                 for (int c = 0; c < half; c += STG_COLS) {
@@ -850,6 +870,19 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
                     tmem_ld32_async(lane_acc + buf * ACC_COLS + c + 32, r[1]);
                     tmem_wait_ld(r[0]);
                     tmem_wait_ld(r[1]);
+                    // 16-bit results of fp32 operands are weight gradients: no activation
+                    if (ACT == SC_ACT_NONE && p.rest) {
+#pragma unroll
+                        for (int h = 0; h < 64; h += 8) {
+                            uint32_t q[8];
+                            tmem_ld8(lane_acc + buf * ACC_COLS + p.rest + c + h, q);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                uint32_t &x = r[h >> 5][(h & 31) + j];
+                                x = __float_as_uint(__uint_as_float(x) + __uint_as_float(q[j]));
+                            }
+                        }
+                    }
                     stage([&](int i) { return __uint_as_float(r[i >> 5][i & 31]); });
                     if (c + STG_COLS >= half) release(buf);
                     store_staged(row0, n0 + c, b, c + STG_COLS < half);
@@ -896,8 +929,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
             tile_at(p, t, tm, tn);
             const int m0 = tm * (CG * GM) + (CG == 2 ? rank * GM : 0);
             const int n0 = tn * p.bn + (CG == 2 ? rank * (p.bn / 2) : 0);
-            int prod = it0 / p.n_k, k = it0 % p.n_k;
-            for (int i = it0; i < it1; ++i, ++issued) {
+            int k = it0, part = 0;
+            for (int i = it0 * p.planes; i < it1 * p.planes; ++i, ++issued) {
                 if (!wait_warp(&sy.empty[r.slot], r.phase ^ 1, abort_flag)) {
                     ok = false;
                     break;
@@ -905,12 +938,12 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
                 if (elect_one()) {
                     const uint32_t sa = base + r.slot * stage_bytes, bar = full0 + r.slot * 8;
                     if (rank == 0 || CG == 1) mbar_expect_tx(&sy.full[r.slot], CG * stage_bytes);
-                    load_tile<CG>(sa, &p.ma, bar, p.a_mn, GM, m0, k * GK, plane_a(prod, p.n_prod));
-                    load_tile<CG>(sa + A_STAGE, &p.mb, bar, p.b_mn, p.bn / CG, n0, k * GK, plane_b(prod, p.n_prod));
+                    load_tile<CG>(sa, &p.ma, bar, p.a_mn, GM, m0, k * GK, part);
+                    load_tile<CG>(sa + A_STAGE, &p.mb, bar, p.b_mn, p.bn / CG, n0, k * GK, part);
                 }
-                if (++k == p.n_k) {
-                    k = 0;
-                    ++prod;
+                if (++part == p.planes) {
+                    part = 0;
+                    ++k;
                 }
                 r.next(p.stages);
             }
@@ -940,26 +973,52 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
             bool ok = true;
             for (int t = first_tile; t < p.n_tiles && ok; t += tile_step) {
                 for (int i = it0; i < it1 && ok; ++n) {
-                    const int buf = n & 1;
-                    if (!wait_warp(&sy.acc_empty[buf], ((n >> 1) & 1) ^ 1, abort_flag)) {
+                    const int buf = n & p.acc_two;
+                    if (!wait_warp(&sy.acc_empty[buf], ((n >> p.acc_two) & 1) ^ 1, abort_flag)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t acc = tmem + buf * ACC_COLS;
                     const int end = min(i + p.chunk, it1);
-                    for (bool first = true; i < end; ++i, first = false) {
-                        if (!wait_warp(&sy.full[r.slot], r.phase, abort_flag)) {
-                            ok = false;
-                            break;
-                        }
+                    // the slot of the next stage, once it is there
+                    auto arrived = [&](int &slot) {
+                        if (!wait_warp(&sy.full[r.slot], r.phase, abort_flag)) return ok = false;
                         tc_fence_after();
+                        slot = r.slot;
+                        r.next(p.stages);
+                        return true;
+                    };
+                    auto product = [&](int a, int b, bool first, int d = 0) {
+                        stage_mmas<CG>(acc + d, da, db, ka, kb, p.idesc, base + a * stage_bytes, base + b * stage_bytes, first);
+                    };
+                    for (bool first = true; i < end; ++i, first = false) {
+                        int s0 = 0, s1 = 0, s2 = 0;
+                        if (!arrived(s0)) break;
+                        if (p.planes == 1) {
+                            if (elect_one()) {
+                                product(s0, s0, first);
+                                mma_commit<CG>(&sy.empty[s0]);
+                                if (i + 1 == end) mma_commit<CG>(&sy.acc_full[buf]);
+                            }
+                            continue;
+                        }
+                        if (elect_one()) product(s0, s0, first);
+                        if (!arrived(s1)) break;
                         if (elect_one()) {
-                            stage_mmas<CG>(acc, da, db, ka, kb, p.idesc, base + r.slot * stage_bytes, first);
-                            mma_commit<CG>(&sy.empty[r.slot]);
+                            product(s1, s0, first, p.rest);
+                            product(s0, s1, false, p.rest);
+                            product(s1, s1, false, p.rest);
+                            mma_commit<CG>(&sy.empty[s1]);
+                        }
+                        if (!arrived(s2)) break;
+                        if (elect_one()) {
+                            product(s2, s0, false, p.rest);
+                            product(s0, s2, false, p.rest);
+                            mma_commit<CG>(&sy.empty[s0]);
+                            mma_commit<CG>(&sy.empty[s2]);
                             if (i + 1 == end) mma_commit<CG>(&sy.acc_full[buf]);
                         }
-                        r.next(p.stages);
                     }
                 }
             }

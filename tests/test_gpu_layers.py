@@ -532,6 +532,17 @@ def test_linear_backward_many_tiles(M, N, K, t, ot):
     check_linear_backward(rnd(g, M, N, dtype=ot), x, w, rnd(g, M, N, dtype=t), "gelu_tanh")
 
 
+@pytest.mark.parametrize("gt", [BF16, F16, F32])
+@pytest.mark.parametrize("M,N,K", [(1300, 3000, 2300), (1300, 1300, 1300), (4300, 130, 70), (65, 520, 1030), (1, 64, 64)])
+def test_linear_backward_f32_operands(M, N, K, gt):
+    """The parts' two accumulators: over several tiles, tiles of either width, shared contractions;
+    weight gradients of 16 bits too."""
+    g = gen(25)
+    x, w = rnd(g, M, K, dtype=F32), rnd(g, N, K, dtype=F32, scale=0.05)
+    check_linear(x, w, rnd(g, N, dtype=F32))
+    check_linear_backward(rnd(g, M, N, dtype=F32), x, w, grad_dtype=gt)
+
+
 def test_linear_backward_options():
     g = gen(23)
     x, w = rnd(g, 130, 72, dtype=BF16), rnd(g, 88, 72, dtype=BF16)
