@@ -84,43 +84,55 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return d;
 }
 
-// Phi, the normal distribution's function, without special functions (16 a
-// clock and SM: an epilogue's few warps would wait for them).  z2 = z^2.  For
-// |z| <= 5.25, Phi(z) = 1/2 + z P(t) with a polynomial of degree 13 in t = 2 z^2 /
-// 5.25^2 - 1 (least squares at Chebyshev nodes, weights adjusted towards equal
-// ripples: off by 0.8e-7, with fp32 roundings 1.7e-7).  Beyond, t stays 1, so
-// 1/2 + z P(1) leaves [0, 1] and saturates to Phi's limits.
-__device__ __forceinline__ float2 normal2(float2 z, float2 z2) {
-    constexpr float A = 5.25f;
-    constexpr float P[14] = {1.346593648e-01f,  -6.712665409e-02f, 4.964389279e-02f,  -3.976862878e-02f, 3.206431866e-02f,
-                             -2.499500290e-02f, 1.832570881e-02f,  -1.295403950e-02f, 9.071036242e-03f,  -5.120746791e-03f,
-                             1.868756372e-03f,  -1.325572259e-03f, 1.456877217e-03f,  -5.612471141e-04f};
-    float2 t = fma2(z2, make_float2(2.f / (A * A), 2.f / (A * A)), make_float2(-1.f, -1.f));
-    t = make_float2(fminf(t.x, 1.f), fminf(t.y, 1.f));
-    float2 h = make_float2(P[13], P[13]);
-#pragma unroll
-    for (int i = 12; i >= 0; --i) h = fma2(h, t, make_float2(P[i], P[i]));
-    return make_float2(__saturatef(fmaf(z.x, h.x, 0.5f)), __saturatef(fmaf(z.y, h.y, 0.5f)));
-}
-
-// gelu(z) = z Phi(z), off by at most 4 * 2^-24 |z|.
-__device__ __forceinline__ float2 gelu2(float2 z) { return mul2(z, normal2(z, mul2(z, z))); }
-
 // 2^x, off by 2^-22 of itself (ex2.approx), 0 far below the normal range.
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// 1 / x, off by 2^-23 of itself; 0 for an infinity.
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Phi, the normal distribution's function, and e = exp(-z^2 / 2).  The lower
+// tail is a product, Phi(-x) = exp(-x^2 / 2) Q(x), and so keeps its relative
+// accuracy; above 0, Phi = 1 - Phi(-z).  Q falls from 1/2 to 1 / (x sqrt(2 pi)),
+// a polynomial of degree 7 in u = 1 / (1 + x / 4) over 0 <= x <= 13.3, where e
+// leaves the normal range (least squares at Chebyshev nodes, weights adjusted
+// towards equal ripples of 2^-20 of itself, 2^-25 in Phi).  With fp32 roundings
+// Phi is off by 2.2e-7 at most and, below 0, by (z^2 + 14) 2^-24 of itself.
+// Two special functions a value (16 a clock and SM) run beside the polynomial's
+// packed steps.
+__device__ __forceinline__ float2 normal2(float2 z, float2 &e) {
+    constexpr float P[8] = {1.706042676e-04f, 9.666055441e-02f,  1.231122538e-01f, -4.171049688e-03f,
+                            3.251675665e-01f, -3.054944277e-01f, 3.596809804e-01f, -9.512647241e-02f};
+    const float2 a = mul2(mul2(z, z), make_float2(-0.72134752f, -0.72134752f));  // -log2(e) / 2
+    e = make_float2(exp2_approx(a.x), exp2_approx(a.y));
+    const float2 u = make_float2(rcp_approx(fmaf(fabsf(z.x), 0.25f, 1.f)), rcp_approx(fmaf(fabsf(z.y), 0.25f, 1.f)));
+    float2 h = make_float2(P[7], P[7]);
+#pragma unroll
+    for (int i = 6; i >= 0; --i) h = fma2(h, u, make_float2(P[i], P[i]));
+    const float2 q = mul2(e, h), r = fma2(q, make_float2(-1.f, -1.f), make_float2(1.f, 1.f));
+    return make_float2(z.x < 0.f ? q.x : r.x, z.y < 0.f ? q.y : r.y);
+}
+
+// gelu(z) = z Phi(z), off by at most 6 * 2^-24 |z| and, below 0, by (z^2 + 16)
+// 2^-24 of itself.
+__device__ __forceinline__ float2 gelu2(float2 z) {
+    float2 e;
+    return mul2(z, normal2(z, e));
+}
 
 // gelu'(z) = Phi(z) + z exp(-z^2 / 2) / sqrt(2 pi); the second term is 0 from
 // |z| = 16 on, which keeps infinity * 0 out.
 __device__ __forceinline__ float2 gelu_grad2(float2 z) {
-    const float2 z2 = mul2(z, z);
-    const float2 a = mul2(z2, make_float2(-0.72134752f, -0.72134752f));  // -log2(e) / 2
-    const float2 e = make_float2(exp2_approx(a.x), exp2_approx(a.y));
+    float2 e;
+    const float2 n = normal2(z, e);
     const float2 c = make_float2(fminf(fmaxf(z.x, -16.f), 16.f), fminf(fmaxf(z.y, -16.f), 16.f));
-    return fma2(mul2(c, make_float2(0.39894228f, 0.39894228f)), e, normal2(z, z2));
+    return fma2(mul2(c, make_float2(0.39894228f, 0.39894228f)), e, n);
 }
 
 // Activations of one value.

@@ -1,0 +1,65 @@
+"""Accuracy of the floating-point layers where elementwise bounds on random sums are too
+wide to see it: activations' tails, exact sums, long sums of one sign.
+
+u = 2^-24 is half a step of fp32, h(t) half a step of a type; every tolerance is the sum of
+the roundings on the way, derived beside it."""
+import math
+
+import pytest
+import torch
+
+from mixed_precision_vit_b200 import sc
+from test_gpu_layers import BF16, F16, F32, U, close, gen, h, phi, rnd, tiny
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- activations -----------------------------------------------------------------------
+def on_values(z, act, out_dtype=None):
+    """act(z) of a vector by a layer with one input and the weight 1: z reaches the activation
+    exactly (one product, nothing to round)."""
+    one = torch.ones(1, 1, dtype=z.dtype, device=z.device)
+    return sc.linear(z[:, None], one, None, None, act, out_dtype=out_dtype)[0][:, 0]
+
+
+def gelu_tail_bound(z):
+    """gelu(z) = z exp(-z^2 / 2) Q, relative to itself: the exponent is rounded three times
+    (3 u z^2 log2(e) / 2 of it, times ln 2), ex2 and rcp are off by 4 u and 2 u, Q moves by its
+    argument's relative error at most 3.2-fold, 7 steps of a polynomial with falling weights
+    round below 8 u, its fit is off by 16 u, and two products round."""
+    return (1.5 * z * z + 4 + 3.2 * 2 + 8 + 16 + 2) * U
+
+
+@pytest.mark.parametrize("t,ot", [(F32, F32), (BF16, F32), (BF16, BF16), (F16, F32), (F16, F16)])
+def test_gelu_keeps_its_lower_tail(t, ot):
+    z = torch.linspace(-12.5, 0, 40001, device="cuda").to(t)
+    y = on_values(z, "gelu", ot)
+    zd = z.double()
+    ref = zd * phi(zd)
+    close(y, ref, gelu_tail_bound(zd) * ref.abs(), "gelu")
+
+
+@pytest.mark.parametrize("t", [F32, BF16, F16])
+def test_gelu_gradient_keeps_its_lower_tail(t):
+    """dbias of one row is dz itself, in fp32: dout gelu'(z) with dout = 1."""
+    z = torch.linspace(-12.5, 0, 40001, device="cuda").to(t)
+    one = torch.ones(1, z.numel(), dtype=t, device="cuda")
+    x, w = torch.ones(1, 8, dtype=t, device="cuda"), torch.ones(z.numel(), 8, dtype=t, device="cuda")
+    db = sc.linear_backward(one, x, w, z[None], "gelu", want_dx=False, want_dw=False, grad_dtype=F32)[2]
+    zd = z.double()
+    p, d = phi(zd), zd * torch.exp(-zd * zd / 2) / math.sqrt(2 * math.pi)
+    close(db, p + d, gelu_tail_bound(zd) * (p + d.abs()), "gelu'")
+
+
+def test_gelu_over_the_whole_range():
+    """Off by 16 u |z| at most in Phi's 1 - q, and right at both ends.  (An infinity comes as a
+    bias: an infinite fp32 operand is an infinity times the other's zero parts, a NaN.)"""
+    ends = torch.tensor([-3e38, 3e38, 1e20, -1e20, 0.0], device="cuda")
+    z = torch.cat([torch.linspace(-20, 20, 60001, device="cuda"), ends])
+    y = on_values(z, "gelu")
+    zd = z.double()
+    assert torch.equal(y[-5:], torch.tensor([0.0, 3e38, 1e20, 0.0, 0.0], device="cuda"))
+    close(y, zd * phi(zd), 16 * U * zd.abs(), "gelu")
+    one = torch.ones(1, 1, device="cuda")
+    assert on_values(torch.tensor([float("nan")], device="cuda"), "gelu").isnan().all()
+    assert sc.linear(one, one, torch.full((1,), math.inf, device="cuda"), None, "gelu")[0].item() == math.inf
