@@ -555,8 +555,9 @@ typedef struct sc_linear_desc {
  * fp32 operands are split into three bf16 parts each (exactly: 3 x 8 bits of
  * significand) whose six leading products are summed in fp32.  bias, act and
  * residual are applied in fp32 and out is rounded once.  The tensor cores cut
- * sums where fp32 arithmetic rounds; where out is SC_F32, sums of at most 1024
- * products are added up in fp32 arithmetic, so that long ones do not drift.
+ * sums where fp32 arithmetic rounds; where out is SC_F32, or a sum has more than
+ * 16384 products, sums of at most 1024 products are added up in fp32 arithmetic,
+ * so that long ones do not drift (weight gradients likewise).
  *   bias       (device, nullable) [N]
  *   residual   (device, nullable) [M][N] of out_type
  *   out        (device) out; may be residual itself (same stride)

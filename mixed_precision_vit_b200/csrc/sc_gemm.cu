@@ -79,7 +79,7 @@ int launch(GemmFn kern, const GemmArgs &p, int grid, int cluster, bool early, cu
 // launched with fewer than the moves add up to, so a build that gave it another
 // number is refused (asked once per kernel).
 bool keep_regs_ok(GemmFn kern) {
-    static std::atomic<GemmFn> known[16];
+    static std::atomic<GemmFn> known[20];  // two tile widths, two types, five activations
     for (auto &k : known)
         if (k.load(std::memory_order_relaxed) == kern) return true;
     cudaFuncAttributes a;
@@ -176,7 +176,9 @@ int launch_gemm(int64_t M, int64_t N, int64_t K, int type16, const GemmOperand &
     p.planes = a.planes;
     p.n_k = (int)div_up(K, GK);
     const Shape sh = choose(M, N, p.n_k, p.planes);
-    p.chunk = epi.out_type != SC_F32 && sh.parts == 1 ? p.n_k : p.planes == 1 ? CHUNK : CHUNK_F32;
+    // one accumulation, or chunks of it added in fp32
+    const int sum = epi.out_type == SC_F32 ? SUM_F32 : p.n_k > LONG_16 ? SUM_16_LONG : SUM_16;
+    p.chunk = sum == SUM_16 && sh.parts == 1 ? p.n_k : p.planes == 1 ? CHUNK : CHUNK_F32;
     // the two accumulators of fp32 operands: twice where two tiles' fit
     p.rest = p.planes == 1 ? 0 : sh.bn <= ACC_COLS / 2 ? ACC_COLS / 2 : ACC_COLS;
     p.acc_two = p.rest < ACC_COLS;
@@ -230,9 +232,9 @@ int launch_gemm(int64_t M, int64_t N, int64_t K, int type16, const GemmOperand &
         default: k = gemm_kernels_none(); break;
     }
     if (sh.parts > 1) return launch(k.split, p, p.n_tiles * sh.parts, sh.parts, early, stream);
-    const int units = sm_count() / sh.cg, keep = epi.out_type == SC_F32;
-    const GemmFn kern = (sh.cg == 2 ? k.pair : k.single)[keep];
-    if (keep && !keep_regs_ok(kern)) {
+    const int units = sm_count() / sh.cg;
+    const GemmFn kern = (sh.cg == 2 ? k.pair : k.single)[sum];
+    if (sum != SUM_16 && !keep_regs_ok(kern)) {
         cudaGetLastError();
         set_error("matrix product: the kernel was built with another number of registers than %d", KEEP_REGS);
         return SC_ERR_CUDA;

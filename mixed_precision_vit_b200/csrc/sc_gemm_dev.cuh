@@ -22,7 +22,9 @@
 // result keeps fp32, an accumulator therefore takes CHUNK steps at most, and
 // the epilogue warps add the chunks in registers (32896 x 1024 x 4096: off by
 // 9.2e-7 of the result's norm, 4.0e-6 in one accumulation; CHUNK / 2 would make
-// it 4.7e-7 in 243 us instead of 230).  fp32 operands keep the five small
+// it 4.7e-7 in 243 us instead of 230).  A 16-bit result's rounding hides the
+// drift of LONG_16 steps (2^-15, half a step of fp16 is 2^-11); longer sums
+// are added up in chunks too.  fp32 operands keep the five small
 // products, below 2^-8 of the result, in an accumulator of their own, so that
 // only the leading product's drift counts, and take CHUNK_F32 steps (8: off by
 // 4.7e-7 where 16 are off by 1.0e-6; 4112 x 4096 x 1024 takes 164 us, 160 with
@@ -69,6 +71,7 @@ constexpr int RING_BYTES = 160 * 1024;  // 5 stages of 32 KB
 constexpr int MAX_RING = 8;
 constexpr int CHUNK = 16;               // steps (1024 indexes) per accumulation of an fp32 result
 constexpr int CHUNK_F32 = 8;            // with fp32 operands
+constexpr int LONG_16 = 256;            // most steps of a 16-bit result in one accumulation
 // Epilogue staging, per warp: 32 rows x 64 columns of fp32, 16-byte quads
 // permuted so that both a lane's row (written) and 8 lanes' row (read) touch
 // every bank once.
@@ -635,11 +638,13 @@ __device__ __forceinline__ void tmem_free(uint32_t base) {
 
 // CG CTAs per tile of CG * 128 rows.  SPLIT (CG = 1): the CTAs of a cluster
 // each take a share of one tile's contraction.  KEEP: the epilogue adds up
-// accumulations of p.chunk stages in registers (fp32 results, and parts).
-template <int CG, bool SPLIT, bool KEEP, int ACT>
+// accumulations of p.chunk steps in registers (fp32 results, parts, long sums).
+// (OUT_ANY for the last two: 32896 x 1024 x 4096 with an fp32 residual and
+// result 273 -> 286 us.)
+template <int CG, bool SPLIT, bool KEEP, int OUT, int ACT>
 __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_constant__ GemmArgs p) {
     static_assert(CG == 1 || !SPLIT, "a shared contraction has one CTA per part");
-    static_assert(KEEP || !SPLIT, "parts are added in fp32");
+    static_assert(KEEP ? SPLIT == (OUT == OUT_ANY) : OUT == OUT_16 && !SPLIT, "parts and fp32 results are added in fp32");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
     uint8_t *ring = smem_raw + (base - smem_addr(smem_raw));
@@ -717,7 +722,6 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
             }
         };
         constexpr int R = 4;  // rows of a lane at a time: lr + 4 k
-        constexpr int OUT = SPLIT ? OUT_ANY : KEEP ? OUT_F32 : OUT_16;
         // 16-bit residuals are loaded one step ahead; fp32 ones (and the sums
         // beside them) would take too many registers
         constexpr bool AHEAD = !KEEP;
@@ -1115,15 +1119,18 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
 using GemmFn = void (*)(GemmArgs);
 
 // The kernels of one activation (sc_gemm_k_*.cu).
+enum { SUM_16, SUM_16_LONG, SUM_F32 };  // result type, and whether its sums are kept in registers
 struct GemmKernels {
-    GemmFn pair[2], single[2];  // [result keeps fp32]
+    GemmFn pair[3], single[3];  // [SUM_*]
     GemmFn split;
 };
 template <int ACT>
 GemmKernels gemm_kernels() {
-    return {{gemm_kernel<2, false, false, ACT>, gemm_kernel<2, false, true, ACT>},
-            {gemm_kernel<1, false, false, ACT>, gemm_kernel<1, false, true, ACT>},
-            gemm_kernel<1, true, true, ACT>};
+    return {{gemm_kernel<2, false, false, OUT_16, ACT>, gemm_kernel<2, false, true, OUT_16, ACT>,
+             gemm_kernel<2, false, true, OUT_F32, ACT>},
+            {gemm_kernel<1, false, false, OUT_16, ACT>, gemm_kernel<1, false, true, OUT_16, ACT>,
+             gemm_kernel<1, false, true, OUT_F32, ACT>},
+            gemm_kernel<1, true, true, OUT_ANY, ACT>};
 }
 GemmKernels gemm_kernels_none();
 GemmKernels gemm_kernels_relu();

@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from mixed_precision_vit_b200 import sc
-from test_gpu_layers import BF16, F16, F32, U, close, gen, h, phi, rnd, tiny
+from test_gpu_layers import BF16, F16, F32, U, check_linear, close, gen, phi, rnd
 
 pytestmark = pytest.mark.gpu
 
@@ -63,3 +63,49 @@ def test_gelu_over_the_whole_range():
     one = torch.ones(1, 1, device="cuda")
     assert on_values(torch.tensor([float("nan")], device="cuda"), "gelu").isnan().all()
     assert sc.linear(one, one, torch.full((1,), math.inf, device="cuda"), None, "gelu")[0].item() == math.inf
+
+
+# ---- long sums -------------------------------------------------------------------------
+def pos(g, *shape, dtype, scale=1.0):
+    return (torch.randn(*shape, device="cuda", generator=g).abs_() * scale).to(dtype)
+
+
+@pytest.mark.parametrize("t", [F16, BF16])
+@pytest.mark.parametrize("N,K", [(2048, 1024), (4096, 1024)])
+def test_long_sums_of_16_bit_results_do_not_drift(N, K, t):
+    """A weight gradient over 262144 rows of one sign, in tiles of either width.  The tensor
+    cores cut at every 16 products, below 2^-22 of the sum so far for all of them together:
+    (1 + .. + 64) / 64 * 2^-22 < 2^-16.9 in a chunk of 1024; 256 chunks add up with half of
+    256 u = 2^-17.  In one accumulation the cuts come to about 2^-11."""
+    g = gen(51)
+    M = 262144
+    x, dout = pos(g, M, K, dtype=t), pos(g, M, N, dtype=t, scale=0.25)
+    w = torch.zeros(N, K, dtype=t, device="cuda")
+    dw = sc.linear_backward(dout, x, w, want_dx=False, want_db=False)[1]
+    n, k = slice(0, N, N // 64 + 1), slice(0, K, K // 64 + 1)
+    ref = dout[:, n].double().t() @ x[:, k].double()
+    close(dw[n, k], ref, 2.0 ** -15.9 * ref, "dw")
+
+
+@pytest.mark.parametrize("gt", [F16, BF16])
+def test_long_weight_gradients_of_fp32_operands(gt):
+    g = gen(52)
+    M, N, K = 20000, 2048, 1024
+    x, dout = rnd(g, M, K), rnd(g, M, N, scale=0.05)
+    w = torch.zeros(N, K, device="cuda")
+    dw = sc.linear_backward(dout, x, w, want_dx=False, want_db=False, grad_dtype=gt)[1]
+    ref, mag = dout.double().t() @ x.double(), dout.double().abs().t() @ x.double().abs()
+    # chunks of 512 products: 32 cuts, (1 + .. + 32) / 32 * 2^-22; the six products leave 3 u out
+    close(dw, ref, (16.5 * 2.0 ** -22 + 20 * U + 4 * U) * mag, "dw")
+
+
+@pytest.mark.parametrize("t", [F16, BF16])
+@pytest.mark.parametrize("M,N", [(2100, 1296), (2100, 1291), (4112, 2048)])
+def test_long_contractions_with_16_bit_results(M, N, t):
+    """Past the longest single accumulation, with every part of the epilogue: aligned and ragged
+    rows, both tile widths."""
+    g = gen(53)
+    K = 16448
+    x, w = rnd(g, M, K, dtype=t), rnd(g, N, K, dtype=t, scale=K ** -0.5)
+    check_linear(x, w, rnd(g, N), rnd(g, M, N, dtype=t), "gelu", want_pre=True)
+    check_linear(x, w)
