@@ -563,7 +563,8 @@ typedef struct sc_linear_desc {
  *   out        (device) out; may be residual itself (same stride)
  *   pre        (device, nullable) out: z rounded to type, for the backward pass
  *   dev_status (device, nullable) receives SC_DEV_WAIT_LIMIT if an internal
- *              bounded wait gave up (outputs are then unspecified)
+ *              bounded wait gave up; the blocks of out and pre that it concerns
+ *              are then NaN, with or without dev_status
  * Non-finite operands give non-finite results in the rows and columns they
  * reach (with fp32 operands an infinity may come out as a NaN).
  * Errors: SC_ERR_ARG (a workspace that is too small among them), SC_ERR_CUDA. */
@@ -578,11 +579,20 @@ int sc_linear(const sc_linear_desc *desc, const void *x, const void *w, const vo
  * same bits.
  *   pre        (device) z from the forward pass; ignored with SC_ACT_NONE
  *   dx, dw, dbias (device, nullable) out, overwritten; an empty sum gives zeros
- *   dev_status as in sc_linear
+ *   dev_status as in sc_linear (the blocks of dx and dw are then NaN)
  * Errors: SC_ERR_ARG (a workspace that is too small among them), SC_ERR_CUDA. */
 int sc_linear_backward(const sc_linear_desc *desc, const void *dout, const void *x, const void *w,
                        const void *pre, void *dx, void *dw, void *dbias, int32_t *dev_status,
                        void *stream);
+
+/* sc_selftest_linear_wait_limit -- exercise what sc_linear does when a bounded
+ * wait gives up (sc_selftest_wait_limit is the wait alone).  Runs sc_linear
+ * without bias and residual, but every wait for a copy of an operand expires
+ * after limit_cycles SM clocks (1 .. 2^34): out and pre become NaN, *dev_status (device, required)
+ * receives SC_DEV_WAIT_LIMIT, and the context stays usable.  Errors as
+ * sc_linear. */
+int sc_selftest_linear_wait_limit(const sc_linear_desc *desc, const void *x, const void *w, void *out,
+                                  void *pre, int64_t limit_cycles, int32_t *dev_status, void *stream);
 
 /* Workspace bytes of the two calls for this problem, or minus an SC_ERR_*
  * status.  The operands' addresses are looked at for their alignment only: a

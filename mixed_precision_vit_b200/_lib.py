@@ -33,7 +33,7 @@ EXPORTS = ("sc_last_error", "sc_version", "sc_kband_tilt", "sc_build_table", "sc
            "sc_bprep_destroy", "sc_selftest_wait_limit",
            "sc_layer_norm", "sc_layer_norm_backward", "sc_layer_norm_workspace_bytes",
            "sc_linear", "sc_linear_backward", "sc_linear_workspace_bytes",
-           "sc_linear_backward_workspace_bytes")
+           "sc_linear_backward_workspace_bytes", "sc_selftest_linear_wait_limit")
 SC_STATIC_WS_BYTES = 64 << 20
 
 
@@ -120,6 +120,7 @@ def load():
         lib.sc_layer_norm_workspace_bytes.restype = ctypes.c_int64
         lib.sc_linear.argtypes = [lin] + [vp] * 8
         lib.sc_linear_backward.argtypes = [lin] + [vp] * 9
+        lib.sc_selftest_linear_wait_limit.argtypes = [lin] + [vp] * 4 + [i64] + [vp] * 2
         lib.sc_linear_workspace_bytes.argtypes = [lin, vp, vp]
         lib.sc_linear_workspace_bytes.restype = ctypes.c_int64
         lib.sc_linear_backward_workspace_bytes.argtypes = [lin, vp, vp, vp]
@@ -322,6 +323,11 @@ def sc_linear_backward(desc: ScLinearDesc, dout, x, w, pre, dx, dw, dbias, dev_s
     _check(load().sc_linear_backward(ctypes.byref(desc), _ptr(dout), _ptr(x), _ptr(w), _ptr(pre),
                                      _ptr(dx), _ptr(dw), _ptr(dbias), _ptr(dev_status),
                                      _stream(stream)))
+
+
+def sc_selftest_linear_wait_limit(desc: ScLinearDesc, x, w, out, pre, limit_cycles, dev_status, stream=None):
+    _check(load().sc_selftest_linear_wait_limit(ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(out), _ptr(pre),
+                                                int(limit_cycles), _ptr(dev_status), _stream(stream)))
 
 
 def sc_linear_workspace_bytes(desc: ScLinearDesc, x, w) -> int:

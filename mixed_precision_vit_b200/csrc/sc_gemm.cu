@@ -171,7 +171,7 @@ Shape choose(int64_t M, int64_t N, int n_k, int planes) {
 
 int launch_gemm(int64_t M, int64_t N, int64_t K, int type16, const GemmOperand &a, const GemmOperand &b,
                 const GemmEpilogue &epi, GemmAfter after, const ColumnSums *sums, int32_t *dev_status,
-                cudaStream_t stream) {
+                cudaStream_t stream, int64_t wait_limit) {
     GemmArgs p;
     p.planes = a.planes;
     p.n_k = (int)div_up(K, GK);
@@ -197,6 +197,9 @@ int launch_gemm(int64_t M, int64_t N, int64_t K, int type16, const GemmOperand &
     p.n_tiles = (int)tiles;
     p.b_stage = sh.bn / sh.cg * GK * 2;
     p.stages = RING_BYTES / (A_STAGE + p.b_stage);
+    // the self-test's copies never bring what their barriers expect
+    p.stage_tx = (uint32_t)(sh.cg * (A_STAGE + p.b_stage)) + (wait_limit > 0 ? 16 : 0);
+    p.wait_limit = wait_limit > 0 ? wait_limit : WAIT_LIMIT_CYCLES;
     if (p.stages > MAX_RING) p.stages = MAX_RING;
     // D fp32; A and B of type16; majorness; N / 8; M / 16
     const uint32_t f = type16 == SC_BF16 ? 1u : 0u;

@@ -41,10 +41,11 @@ enum GemmAfter {
     BESIDE_GEMM,  // another product of the same passes: runs on the SMs which that one leaves
 };
 
-// sums (nullable): finished by a warp that the product leaves idle.
+// sums (nullable): finished by a warp that the product leaves idle.  wait_limit >
+// 0: the self-test, whose waits for copies all expire after so many cycles.
 int launch_gemm(int64_t M, int64_t N, int64_t K, int type16, const GemmOperand &a,
                 const GemmOperand &b, const GemmEpilogue &epi, GemmAfter after,
-                const ColumnSums *sums, int32_t *dev_status, cudaStream_t stream);
+                const ColumnSums *sums, int32_t *dev_status, cudaStream_t stream, int64_t wait_limit = 0);
 
 // ---- activations ------------------------------------------------------------
 // 1 / (1 + exp(-x)) times n.  The intrinsics' errors (2 ulp of the quotient, a

@@ -46,9 +46,10 @@
 // pre-activation kept, where the epilogue sets the pace (tensor pipe 55 % busy);
 // 32896 x 1024 x 4096 with an fp32 residual and result 216 (tensor pipe 79 %;
 // cuBLAS 195 without either).
-// All waits are bounded, as in the count engine: on expiry the kernel records
-// SC_DEV_WAIT_LIMIT, waits for its own copies and products, frees tensor
-// memory and returns.
+// All waits are bounded, as in the count engine.  A CTA (a pair, a cluster that
+// shares a tile) whose wait expires waits for its own copies and products,
+// writes NaN over its tiles, records SC_DEV_WAIT_LIMIT, frees tensor memory and
+// returns.
 #pragma once
 #include <cuda.h>
 
@@ -106,6 +107,8 @@ struct GemmArgs {
     int beside;         // BESIDE_GEMM
     ColumnSums sums;    // part null: none
     uint32_t idesc;
+    uint32_t stage_tx;  // bytes that a stage's copies bring, both CTAs' of a pair
+    long long wait_limit;
     int bias_type, out_type, pre_type;
     int vec;            // 8 columns per access everywhere
 };
@@ -116,6 +119,8 @@ struct GemmSync {
     uint64_t drain;
     uint32_t tmem_base;
     int abort_flag;
+    uint32_t issued;                   // stages that this CTA's copies were issued for
+    uint32_t peer_issued, peer_abort;  // the same of a pair's other CTA, and whether it gave up
 };
 
 constexpr int GEMM_SMEM = RING_BYTES + EPI_WARPS * STG_BYTES + 1024 + 512;
@@ -194,6 +199,14 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t saddr, uint32_t rank) 
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
     return r;
+}
+
+__device__ __forceinline__ void store_cluster(const void *where, uint32_t rank, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(smem_addr(where), rank)), "r"(v) : "memory");
+}
+// Takes n bytes off what a barrier still expects.
+__device__ __forceinline__ void mbar_complete_tx(uint64_t *bar, uint32_t n) {
+    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(n) : "memory");
 }
 
 // Row and column of tile t.  Tiles run down GROUP_M row tiles before the next
@@ -673,6 +686,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
         }
         mbar_init(&sy.drain, 1);
         sy.abort_flag = 0;
+        sy.issued = sy.peer_issued = sy.peer_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 2) tmem_alloc<CG>(&sy.tmem_base);
@@ -686,6 +700,9 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
     if (!p.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int stage_bytes = A_STAGE + p.b_stage;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.wait_limit));
+    };
     auto epilogue = [&]() {
         // ================= epilogue =================
         // Warps e and e + 4 share a quadrant of tensor-memory lanes (32 rows)
@@ -826,7 +843,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
                 float v[COLS] = {};
                 for (int i = it0; i < it1; i += p.chunk, ++n) {
                     const int buf = n & p.acc_two;
-                    if (!wait_warp(&sy.acc_full[buf], (n >> p.acc_two) & 1, abort_flag)) return;
+                    if (!wait(&sy.acc_full[buf], (n >> p.acc_two) & 1)) return;
                     tc_fence_after();
                     uint32_t acc = lane_acc + buf * ACC_COLS + p.rest;
                     for (int left = p.rest;; left = 0, acc -= p.rest) {  // the rest first
@@ -862,7 +879,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
                 }
             } else {
                 const int buf = n & p.acc_two;
-                if (!wait_warp(&sy.acc_full[buf], (n >> p.acc_two) & 1, abort_flag)) return;
+                if (!wait(&sy.acc_full[buf], (n >> p.acc_two) & 1)) return;
                 ++n;
                 tc_fence_after();
                 for (int c = 0; c < half; c += STG_COLS) {
@@ -894,16 +911,69 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
             }
         }
     };
+    // After a wait that expired: this CTA's (a pair's) products finish and its
+    // copies land, each waited for with a limit again.  All threads call it, of
+    // both CTAs of a pair, with no product or copy left to issue.
+    auto settle = [&]() {
+        int unused = 0;
+        const long long limit = p.wait_limit / 16;
+        if (warp == 1) {
+            if ((CG == 1 || rank == 0) && elect_one()) mma_commit<CG>(&sy.drain);  // arrives in both CTAs
+            mbar_wait(&sy.drain, 0, &unused, limit);
+        } else if (threadIdx.x == 0 && rank * (CG - 1) == 0) {
+            // A pair's copies all count on this CTA's barriers, which expect
+            // both halves of the stages that this CTA armed: what only one of
+            // the two issued is put right first.
+            const uint32_t mine = sy.issued, other = CG == 2 ? sy.peer_issued : mine;
+            const uint32_t end = max(mine, other), n = p.stages;
+            for (uint32_t j = end < n ? 0 : end - n; j < end; ++j) {
+                uint64_t *bar = &sy.full[j % n];
+                if (j >= mine) mbar_expect_tx(bar, stage_bytes);
+                else if (j >= other) mbar_complete_tx(bar, stage_bytes);
+                unused = 0;
+                mbar_wait(bar, (j / n) & 1, &unused, limit);
+            }
+        }
+        __syncwarp();
+        __syncthreads();
+    };
     // all products and copies done, no arrival on its way to another CTA
     auto finish = [&]() {
         tc_fence_before();
         __syncthreads();
+        if (CG == 2 && threadIdx.x == 0) {
+            if (rank == 1) store_cluster(&sy.peer_issued, 0, sy.issued);
+            if (*abort_flag) store_cluster(&sy.peer_abort, rank ^ 1, 1);
+        }
+        __syncwarp();
         if (CG == 2 || SPLIT) cluster_sync();
         tc_fence_after();
+        if (__builtin_expect(*abort_flag || (CG == 2 && *(volatile uint32_t *)&sy.peer_abort), 0)) {
+            if (!SPLIT) {
+                settle();
+                // no result of this CTA can be told from a right one: NaN (asks
+                // for its place again: the usual way keeps no registers for this)
+                const int step = CG == 2 ? (int)cluster_count() : (int)gridDim.x;
+                for (int t = CG == 2 ? (int)cluster_id() : (int)blockIdx.x; t < p.n_tiles; t += step) {
+                    int tm, tn;
+                    tile_at(p, t, tm, tn);
+                    const int64_t row0 = ((int64_t)tm * CG + (CG == 2 ? cluster_rank() : 0)) * GM;
+                    for (int i = threadIdx.x; i < GM * p.bn; i += GEMM_THREADS) {
+                        const int64_t row = row0 + i / p.bn;
+                        const int col = tn * p.bn + i % p.bn;
+                        if (row >= p.M || col >= p.N) continue;
+                        if (p.pre) store_any(p.pre, p.pre_type, row * p.ld_pre + col, NAN);
+                        store_any(p.out, p.out_type, row * p.ld_out + col, NAN);
+                    }
+                }
+            }
+            if (threadIdx.x == 0 && p.dev_status) atomicOr(p.dev_status, SC_DEV_WAIT_LIMIT);
+            __syncwarp();
+            if (CG == 2) cluster_sync();
+        }
         if (warp == 2) tmem_free<CG>(tmem);
         // what follows on the stream must find the other product done too
         if (p.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
-        if (threadIdx.x == 0 && sy.abort_flag && p.dev_status) atomicOr(p.dev_status, SC_DEV_WAIT_LIMIT);
     };
     // 128 sums per epilogue thread: those warps take registers over from the
     // other four (launched with KEEP_REGS each, which the host checks: 56 + 2 x
@@ -935,13 +1005,13 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
             const int n0 = tn * p.bn + (CG == 2 ? rank * (p.bn / 2) : 0);
             int k = it0, part = 0;
             for (int i = it0 * p.planes; i < it1 * p.planes; ++i, ++issued) {
-                if (!wait_warp(&sy.empty[r.slot], r.phase ^ 1, abort_flag)) {
+                if (!wait(&sy.empty[r.slot], r.phase ^ 1)) {
                     ok = false;
                     break;
                 }
                 if (elect_one()) {
                     const uint32_t sa = base + r.slot * stage_bytes, bar = full0 + r.slot * 8;
-                    if (rank == 0 || CG == 1) mbar_expect_tx(&sy.full[r.slot], CG * stage_bytes);
+                    if (rank == 0 || CG == 1) mbar_expect_tx(&sy.full[r.slot], p.stage_tx);
                     load_tile<CG>(sa, &p.ma, bar, p.a_mn, GM, m0, k * GK, part);
                     load_tile<CG>(sa + A_STAGE, &p.mb, bar, p.b_mn, p.bn / CG, n0, k * GK, part);
                 }
@@ -952,19 +1022,13 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
                 r.next(p.stages);
             }
         }
-        // the last copies of the ring, oldest first
-        const uint32_t last = issued < (uint32_t)p.stages ? issued : p.stages;
-        r.back(last, p.stages);
-        Ring q = r;
+        if (lane == 0) sy.issued = issued;
         if (ok) {
-            // every stage consumed: no copy and no arrival is in flight
-            for (uint32_t j = 0; j < last; ++j, q.next(p.stages)) wait_warp(&sy.empty[q.slot], q.phase, abort_flag);
-        }
-        if (*abort_flag && (rank == 0 || CG == 1)) {
-            // gave up: let the copies that were issued land
-            int dummy = 0;
-            for (uint32_t j = 0; j < last; ++j, r.next(p.stages))
-                mbar_wait(&sy.full[r.slot], r.phase, &dummy, WAIT_LIMIT_CYCLES / 16);
+            // the ring's last stages consumed, oldest first: no copy and no
+            // arrival is in flight
+            const uint32_t last = issued < (uint32_t)p.stages ? issued : p.stages;
+            r.back(last, p.stages);
+            for (uint32_t j = 0; j < last; ++j, r.next(p.stages)) wait(&sy.empty[r.slot], r.phase);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -978,7 +1042,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
             for (int t = first_tile; t < p.n_tiles && ok; t += tile_step) {
                 for (int i = it0; i < it1 && ok; ++n) {
                     const int buf = n & p.acc_two;
-                    if (!wait_warp(&sy.acc_empty[buf], ((n >> p.acc_two) & 1) ^ 1, abort_flag)) {
+                    if (!wait(&sy.acc_empty[buf], ((n >> p.acc_two) & 1) ^ 1)) {
                         ok = false;
                         break;
                     }
@@ -987,7 +1051,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
                     const int end = min(i + p.chunk, it1);
                     // the slot of the next stage, once it is there
                     auto arrived = [&](int &slot) {
-                        if (!wait_warp(&sy.full[r.slot], r.phase, abort_flag)) return ok = false;
+                        if (!wait(&sy.full[r.slot], r.phase)) return ok = false;
                         tc_fence_after();
                         slot = r.slot;
                         r.next(p.stages);
@@ -1026,11 +1090,6 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
                     }
                 }
             }
-            if (*abort_flag) {  // gave up: let the products that were issued finish
-                int dummy = 0;
-                if (elect_one()) mma_commit<CG>(&sy.drain);
-                mbar_wait(&sy.drain, 0, &dummy, WAIT_LIMIT_CYCLES / 16);
-            }
         }
         __syncwarp();
     } else if (warp == 3) {
@@ -1064,50 +1123,53 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
         // every part is in its CTA's shared memory: add them up, a share of
         // the rows each
         __syncthreads();
+        if (__builtin_expect(*abort_flag, 0)) {  // NaN in this part makes the sums NaN
+            settle();
+            for (int i = threadIdx.x; i < GM * SPLIT_LD; i += GEMM_THREADS) reinterpret_cast<float *>(ring)[i] = NAN;
+            __syncthreads();
+        }
         cluster_sync();
         const int parts = (int)gridDim.x / p.n_tiles;
         int tm, tn;
         tile_at(p, first_tile, tm, tn);
         const int m0 = tm * GM, n0 = tn * p.bn;
         const int groups = p.bn / 8;
-        if (!*abort_flag) {
-            const int r0 = GM * rank / parts, r1 = GM * (rank + 1) / parts;
-            for (int i = threadIdx.x; i < (r1 - r0) * groups; i += GEMM_THREADS) {
-                const int r = r0 + i / groups, c = (i % groups) * 8;
-                if (m0 + r >= p.M || n0 + c >= p.N) continue;
-                float v[8] = {};
-                const uint32_t mine = base + (uint32_t)(r * SPLIT_LD + c) * 4;
-                for (int q = 0; q < parts; ++q) {
-                    const uint32_t at = cluster_addr(mine, q);
-                    float a[8];
-                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                 : "=f"(a[0]), "=f"(a[1]), "=f"(a[2]), "=f"(a[3])
-                                 : "r"(at));
-                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                 : "=f"(a[4]), "=f"(a[5]), "=f"(a[6]), "=f"(a[7])
-                                 : "r"(at + 16));
+        const int r0 = GM * rank / parts, r1 = GM * (rank + 1) / parts;
+        for (int i = threadIdx.x; i < (r1 - r0) * groups; i += GEMM_THREADS) {
+            const int r = r0 + i / groups, c = (i % groups) * 8;
+            if (m0 + r >= p.M || n0 + c >= p.N) continue;
+            float v[8] = {};
+            const uint32_t mine = base + (uint32_t)(r * SPLIT_LD + c) * 4;
+            for (int q = 0; q < parts; ++q) {
+                const uint32_t at = cluster_addr(mine, q);
+                float a[8];
+                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(a[0]), "=f"(a[1]), "=f"(a[2]), "=f"(a[3])
+                             : "r"(at));
+                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(a[4]), "=f"(a[5]), "=f"(a[6]), "=f"(a[7])
+                             : "r"(at + 16));
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] += a[j];
-                }
-                if (p.vec) {
-                    float b[8] = {};
-                    if (p.bias) load_any<8>(p.bias, p.bias_type, n0 + c, b);
-                    float o[1][8];
+                for (int j = 0; j < 8; ++j) v[j] += a[j];
+            }
+            if (p.vec) {
+                float b[8] = {};
+                if (p.bias) load_any<8>(p.bias, p.bias_type, n0 + c, b);
+                float o[1][8];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) o[0][j] = v[j];
-                    const bool in[1] = {true};
-                    const RowPtrs q = row_ptrs(p, m0 + r, n0 + c);
-                    Residual<1, OUT_ANY> a;
-                    if (p.res) a.load(p, q.res, 0, in);
-                    epilogue_rows<ACT, OUT_ANY, 1>(p, o, b, a, q, 0, in);
-                } else {
+                for (int j = 0; j < 8; ++j) o[0][j] = v[j];
+                const bool in[1] = {true};
+                const RowPtrs q = row_ptrs(p, m0 + r, n0 + c);
+                Residual<1, OUT_ANY> a;
+                if (p.res) a.load(p, q.res, 0, in);
+                epilogue_rows<ACT, OUT_ANY, 1>(p, o, b, a, q, 0, in);
+            } else {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        if (n0 + c + j >= p.N) break;
-                        float b[1] = {0.f};
-                        if (p.bias) load_any<1>(p.bias, p.bias_type, n0 + c + j, b);
-                        epilogue1<ACT>(p, v[j], b[0], m0 + r, n0 + c + j);
-                    }
+                for (int j = 0; j < 8; ++j) {
+                    if (n0 + c + j >= p.N) break;
+                    float b[1] = {0.f};
+                    if (p.bias) load_any<1>(p.bias, p.bias_type, n0 + c + j, b);
+                    epilogue1<ACT>(p, v[j], b[0], m0 + r, n0 + c + j);
                 }
             }
         }

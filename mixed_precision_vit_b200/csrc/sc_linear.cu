@@ -382,11 +382,9 @@ extern "C" int64_t sc_linear_backward_workspace_bytes(const sc_linear_desc *d, c
     return d->M == 0 || d->N == 0 ? 0 : bwd_workspace(*d, dout, x, w);
 }
 
-extern "C" int sc_linear(const sc_linear_desc *d, const void *x, const void *w, const void *bias,
-                         const void *residual, void *out, void *pre, int32_t *dev_status,
-                         void *stream) {
-    const char *who = "sc_linear";
-    clear_error();
+// wait_limit: see launch_gemm
+static int linear(const char *who, const sc_linear_desc *d, const void *x, const void *w, const void *bias,
+                  const void *residual, void *out, void *pre, int32_t *dev_status, void *stream, int64_t wait_limit) {
     if (int rc = check_desc(d, who)) return rc;
     if (bias && !type_ok(d->bias_type)) {
         set_error("%s: bias_type %d", who, d->bias_type);
@@ -421,7 +419,26 @@ extern "C" int sc_linear(const sc_linear_desc *d, const void *x, const void *w, 
     e.out_type = d->out_type;
     e.pre_type = d->type;
     e.act = d->act;
-    return launch_gemm(d->M, d->N, d->K, tc_type(d->type), a, b, e, passes.a.n ? AFTER_PASS : AFTER_ANY, nullptr, dev_status, s);
+    return launch_gemm(d->M, d->N, d->K, tc_type(d->type), a, b, e, passes.a.n ? AFTER_PASS : AFTER_ANY, nullptr, dev_status, s,
+                       wait_limit);
+}
+
+extern "C" int sc_linear(const sc_linear_desc *d, const void *x, const void *w, const void *bias,
+                         const void *residual, void *out, void *pre, int32_t *dev_status,
+                         void *stream) {
+    clear_error();
+    return linear("sc_linear", d, x, w, bias, residual, out, pre, dev_status, stream, 0);
+}
+
+extern "C" int sc_selftest_linear_wait_limit(const sc_linear_desc *d, const void *x, const void *w, void *out, void *pre,
+                                             int64_t limit_cycles, int32_t *dev_status, void *stream) {
+    const char *who = "sc_selftest_linear_wait_limit";
+    clear_error();
+    if (!dev_status || limit_cycles < 1 || limit_cycles > (int64_t)1 << 34) {
+        set_error("%s: dev_status is null, or limit %lld outside [1, 2^34] cycles", who, (long long)limit_cycles);
+        return SC_ERR_ARG;
+    }
+    return linear(who, d, x, w, nullptr, nullptr, out, pre, dev_status, stream, limit_cycles);
 }
 
 extern "C" int sc_linear_backward(const sc_linear_desc *d, const void *dout, const void *x,

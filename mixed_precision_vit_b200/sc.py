@@ -410,7 +410,9 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias=None, residual=None, act="none
     out_dtype, which is x's type (default) or float32.  act: a key of ACTIVATIONS.  pre
     is x w^T + bias in x's type with want_pre (what linear_backward needs for an
     activation), else None.  out: the tensor to write, which may be the residual.
-    workspace: device scratch of sc_linear_workspace_bytes, allocated when None."""
+    workspace: device scratch of sc_linear_workspace_bytes, allocated when None.
+    dev_status: int32 tensor that receives SC_DEV_WAIT_LIMIT if an internal wait gave up;
+    the blocks of out and pre that it concerns are then NaN, with or without it."""
     M, K, ld_x = _matrix(x, "x")
     dev = x.get_device()
     if stream is not None or dev != torch.cuda.current_device():
