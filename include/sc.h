@@ -597,7 +597,9 @@ int sc_selftest_linear_wait_limit(const sc_linear_desc *desc, const void *x, con
 /* Workspace bytes of the two calls for this problem, or minus an SC_ERR_*
  * status.  The operands' addresses are looked at for their alignment only: a
  * 16-bit operand whose rows do not start on 16-byte boundaries is copied into
- * the workspace, an fp32 operand is split there.  Host only. */
+ * the workspace, an fp32 operand is split there.  An operand that is NULL here is
+ * one that the call does not read (x without dw, w without dx) and takes no
+ * room; with both NULL, dbias alone is wanted.  Host only. */
 int64_t sc_linear_workspace_bytes(const sc_linear_desc *desc, const void *x, const void *w);
 int64_t sc_linear_backward_workspace_bytes(const sc_linear_desc *desc, const void *dout,
                                            const void *x, const void *w);

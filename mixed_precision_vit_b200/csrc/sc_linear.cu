@@ -346,9 +346,10 @@ int check_workspace(const sc_linear_desc &d, int64_t need, const char *who) {
     return SC_OK;
 }
 
+// What the copies of x and w take; a null operand is not read.
 int64_t fwd_workspace(const sc_linear_desc &d, const void *x, const void *w) {
-    return (in_place(x, d.ld_x, d.type) ? 0 : copy_bytes(d.M, d.K, d.type)) +
-           (in_place(w, d.ld_w, d.type) ? 0 : copy_bytes(d.N, d.K, d.type));
+    return (!x || in_place(x, d.ld_x, d.type) ? 0 : copy_bytes(d.M, d.K, d.type)) +
+           (!w || in_place(w, d.ld_w, d.type) ? 0 : copy_bytes(d.N, d.K, d.type));
 }
 
 // dz is dout itself
@@ -360,8 +361,10 @@ int64_t part_bytes(const sc_linear_desc &d) {
     return round_up((int64_t)pass_chunks(d.M, d.N, true) * d.N * (int64_t)sizeof(float), 256);
 }
 
-int64_t bwd_workspace(const sc_linear_desc &d, const void *dout, const void *x, const void *w) {
-    return part_bytes(d) + (dz_in_place(d, dout) ? 0 : copy_bytes(d.M, d.N, d.type)) + fwd_workspace(d, x, w);
+// x: null unless dw is wanted, w: null unless dx is; sums: dbias is wanted.
+int64_t bwd_workspace(const sc_linear_desc &d, const void *dout, const void *x, const void *w, bool sums) {
+    return (sums ? part_bytes(d) : 0) + ((!x && !w) || dz_in_place(d, dout) ? 0 : copy_bytes(d.M, d.N, d.type)) +
+           fwd_workspace(d, x, w);
 }
 
 }  // namespace
@@ -379,7 +382,7 @@ extern "C" int64_t sc_linear_backward_workspace_bytes(const sc_linear_desc *d, c
                                                       const void *x, const void *w) {
     clear_error();
     if (int rc = check_desc(d, "sc_linear_backward_workspace_bytes")) return -rc;
-    return d->M == 0 || d->N == 0 ? 0 : bwd_workspace(*d, dout, x, w);
+    return d->M == 0 || d->N == 0 ? 0 : bwd_workspace(*d, dout, x, w, true);
 }
 
 // wait_limit: see launch_gemm
@@ -465,7 +468,7 @@ extern "C" int sc_linear_backward(const sc_linear_desc *d, const void *dout, con
         if (int rc = check_matrix(dx ? w : nullptr, d->ld_w, d->K, who, "w")) return rc;
         if (int rc = check_matrix(dw ? x : nullptr, d->ld_x, d->K, who, "x")) return rc;
         if (int rc = check_matrix(pre, d->ld_pre, d->N, who, "pre")) return rc;
-        if (int rc = check_workspace(*d, bwd_workspace(*d, dout, x, w), who)) return rc;
+        if (int rc = check_workspace(*d, bwd_workspace(*d, dout, dw ? x : nullptr, dx ? w : nullptr, dbias), who)) return rc;
     } else {
         // an empty sum: zeros
         cudaError_t e = cudaSuccess;
@@ -485,16 +488,15 @@ extern "C" int sc_linear_backward(const sc_linear_desc *d, const void *dout, con
     p.ld_pre = d->ld_pre;
     p.in = dout;
     p.pre = pre;
-    float *part = static_cast<float *>(ws.take(part_bytes(*d)));
-    p.part = dbias ? part : nullptr;
+    if (dbias) p.part = static_cast<float *>(ws.take(part_bytes(*d)));
     GemmOperand dz = {};
     if (dz_in_place(*d, dout)) {
         dz.p = dout;
         dz.ld = d->ld_out;
         dz.planes = 1;
-    } else {
+    } else if (dx || dw) {
         dz = copied(ws.take(copy_bytes(d->M, d->N, d->type)), d->M, d->N, d->type);
-        if (dx || dw) p.dst = const_cast<void *>(dz.p);
+        p.dst = const_cast<void *>(dz.p);
         p.ld_dst = dz.ld;
         p.plane = dz.plane_stride;
     }
@@ -504,7 +506,7 @@ extern "C" int sc_linear_backward(const sc_linear_desc *d, const void *dout, con
     if (dw) bx = operand(x, d->M, d->K, d->ld_x, d->type, false, ws, passes);
     if (int rc = passes.launch(d->type, s)) return rc;
     if (dbias) {
-        sums.part = part;
+        sums.part = p.part;
         sums.n = passes.a.job[0].chunks;
         sums.cols = d->N;
         sums.out = dbias;

@@ -484,7 +484,7 @@ def linear_backward(dout: torch.Tensor, x: torch.Tensor, w: torch.Tensor, pre=No
     d = L.ScLinearDesc(M, N, K, ld_x, ld_w, ld_out, 0, ld_pre, K, K, _type(xt, "x"),
                        _type(dout.dtype, "dout"), 0, _type(gt, "grad_dtype"), code)
     lib = L.lib()
-    dp, xp, wp = dout.data_ptr(), x.data_ptr(), w.data_ptr()
+    dp, xp, wp = dout.data_ptr(), x.data_ptr() if want_dw else None, w.data_ptr() if want_dx else None
     ws = _scratch(d, L.check_bytes(lib.sc_linear_backward_workspace_bytes(d, dp, xp, wp)), workspace, x)
     L.check(lib.sc_linear_backward(d, dp, xp, wp, _ptr(pre) if code else None, _ptr(dx), _ptr(dw),
                                    _ptr(db), _status(dev_status, dev), _raw_stream(dev)))

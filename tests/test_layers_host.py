@@ -31,3 +31,34 @@ def test_wait_limit_selftest_refuses(lib):
         assert L.sc_last_error().startswith("sc_selftest_linear_wait_limit:")
     d = _linear(ld_out=15)
     assert lib.sc_selftest_linear_wait_limit(ctypes.byref(d), P, P, P, P, 1000, P, None) == L.SC_ERR_ARG
+
+
+@pytest.mark.parametrize("t", [L.SC_BF16, L.SC_F32])
+def test_backward_workspace_counts_what_the_call_reads(lib, t):
+    """dz, x and w take room (6 bytes an element here: three planes, or one copy of rows off their
+    boundaries and their padding) only where a wanted output needs them."""
+    M, N, K, size = 40, 24, 56, 6 if t == L.SC_F32 else 2
+    kw = dict(M=M, N=N, K=K, type=t, out_type=t, ld_x=K + 1, ld_w=K + 1, ld_out=N + 1)
+    q = lambda x, w: L.sc_linear_backward_workspace_bytes(_linear(**kw), P, x, w)
+    up = lambda n: (n + 255) // 256 * 256
+    sums, dz = q(None, None), up(M * N * size)
+    assert 0 < sums <= up(256 * N * 4)
+    assert q(None, P) == sums + dz + up(N * K * size)
+    assert q(P, None) == sums + dz + up(M * K * size)
+    assert q(P, P) == sums + dz + up(N * K * size) + up(M * K * size)
+
+
+def test_backward_asks_for_no_more_than_the_outputs_need(lib):
+    """Calls refused for a workspace of 64 bytes name the bytes that they need: nothing for operands
+    that they do not read, whatever stands in those operands' strides."""
+    dz, x, w = 256, 512, 2048  # 4 x 16, 4 x 64 and 16 x 64 bf16
+    part = L.sc_linear_backward_workspace_bytes(_linear(), P, None, None)
+    kw = dict(ld_out=17, workspace=P, workspace_bytes=64)
+    for ops, outs, strides, need in (((None, P), (P, None, None), dict(ld_x=3), dz),
+                                     ((P, None), (None, P, None), dict(ld_w=3), dz),
+                                     ((P, P), (None, P, P), dict(ld_x=65, ld_w=3), dz + x + part),
+                                     ((P, P), (P, None, None), dict(ld_x=3, ld_w=65), dz + w),
+                                     ((None, None), (None, None, P), dict(ld_x=3, ld_w=5), part)):
+        d = _linear(**{**kw, **strides})
+        rc = lib.sc_linear_backward(ctypes.byref(d), P, *ops, None, *outs, None, None)
+        assert rc == L.SC_ERR_ARG and f"{need} needed" in L.sc_last_error(), (L.sc_last_error(), need)
