@@ -146,17 +146,20 @@ __device__ __forceinline__ float act_fn(float z) {
     return z;
 }
 
+// The terms that vanish at both ends are 0 in fp32 from the bounds below on
+// (q (1 - q) of gelu_tanh from |z| = 16, silu's q or 1 - q from 128), which keep
+// infinity * 0 out.
 template <int ACT>
 __device__ __forceinline__ float act_grad(float z) {
     if constexpr (ACT == SC_ACT_RELU) return z > 0.f ? 1.f : (z == z ? 0.f : z);
     if constexpr (ACT == SC_ACT_GELU) return gelu_grad2(make_float2(z, z)).x;
     if constexpr (ACT == SC_ACT_GELU_TANH) {
-        const float q = times_sigmoid(1.f, gelu_tanh_arg(z));
-        return q + z * q * (1.f - q) * 1.59576912f * (1.f + 0.134145f * z * z);
+        const float q = times_sigmoid(1.f, gelu_tanh_arg(z)), c = fminf(fmaxf(z, -16.f), 16.f);
+        return q + c * q * (1.f - q) * 1.59576912f * (1.f + 0.134145f * c * c);
     }
     if constexpr (ACT == SC_ACT_SILU) {
-        const float q = times_sigmoid(1.f, z);
-        return q * (1.f + z * (1.f - q));
+        const float q = times_sigmoid(1.f, z), c = fminf(fmaxf(z, -128.f), 128.f);
+        return q * (1.f + c * (1.f - q));
     }
     return 1.f;
 }

@@ -65,6 +65,19 @@ def test_gelu_over_the_whole_range():
     assert sc.linear(one, one, torch.full((1,), math.inf, device="cuda"), None, "gelu")[0].item() == math.inf
 
 
+@pytest.mark.parametrize("t", [F32, BF16, F16])
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+def test_gradients_of_saturated_activations(act, t):
+    """Far from 0 the derivative is 0 or 1, also where a pre-activation was kept as an infinity
+    (fp16 from 65520 on)."""
+    top = torch.finfo(t).max
+    z = torch.tensor([200.0, 6e4, top, math.inf, -200.0, -6e4, -top, -math.inf, 1e20, -1e20, math.nan], device="cuda").to(t)
+    one = torch.ones(1, z.numel(), dtype=t, device="cuda")
+    x, w = torch.ones(1, 8, dtype=t, device="cuda"), torch.ones(z.numel(), 8, dtype=t, device="cuda")
+    db = sc.linear_backward(one, x, w, z[None], act, want_dx=False, want_dw=False, grad_dtype=F32)[2]
+    assert torch.equal(db[:-1], (z[:-1] > 0).float()) and db[-1].isnan()
+
+
 # ---- long sums -------------------------------------------------------------------------
 def pos(g, *shape, dtype, scale=1.0):
     return (torch.randn(*shape, device="cuda", generator=g).abs_() * scale).to(dtype)
