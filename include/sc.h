@@ -532,7 +532,8 @@ int64_t sc_layer_norm_workspace_bytes(const sc_norm_desc *desc);
  *   grad_type  of dw and dbias: any (type is what an optimiser in type wants)
  * A stride or type that belongs to no pointer of the call is ignored. */
 typedef struct sc_linear_desc {
-    int64_t M, N, K;   /* 0 <= M, N and 1 <= K, each < 2^31                    */
+    int64_t M, N, K;   /* 0 <= M, N and 1 <= K, each < 2^31, and no matrix of
+                        * more than 2^56 elements                              */
     int64_t ld_x;      /* >= K: x [M][K]                                       */
     int64_t ld_w;      /* >= K: w [N][K]                                       */
     int64_t ld_out;    /* >= N: out or dout [M][N]                             */

@@ -314,6 +314,13 @@ int check_desc(const sc_linear_desc *d, const char *who) {
                   (long long)d->M, (long long)d->N, (long long)d->K);
         return SC_ERR_ARG;
     }
+    // more than any address space holds, and what workspace sizes could not count
+    constexpr int64_t MOST = (int64_t)1 << 56;
+    if (d->M * d->N > MOST || d->M * d->K > MOST || d->N * d->K > MOST) {
+        set_error("%s: a matrix of more than 2^56 elements (M %lld, N %lld, K %lld)", who, (long long)d->M, (long long)d->N,
+                  (long long)d->K);
+        return SC_ERR_ARG;
+    }
     if (!type_ok(d->type) || !type_ok(d->out_type) || (d->out_type != d->type && d->out_type != SC_F32)) {
         set_error("%s: type %d with out_type %d", who, d->type, d->out_type);
         return SC_ERR_ARG;

@@ -62,3 +62,19 @@ def test_backward_asks_for_no_more_than_the_outputs_need(lib):
         d = _linear(**{**kw, **strides})
         rc = lib.sc_linear_backward(ctypes.byref(d), P, *ops, None, *outs, None, None)
         assert rc == L.SC_ERR_ARG and f"{need} needed" in L.sc_last_error(), (L.sc_last_error(), need)
+
+
+@pytest.mark.parametrize("M,N,K", [(2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31 - 1, 1, 2 ** 31 - 1),
+                                   (1, 2 ** 31 - 1, 2 ** 26), (2 ** 30, 2 ** 27, 1)])
+def test_sizes_that_no_byte_count_holds_are_refused(lib, M, N, K):
+    """The workspace's bytes passed 2^63 there, and their sum could come out small."""
+    for t in (L.SC_F32, L.SC_BF16):
+        kw = dict(M=M, N=N, K=K, type=t, out_type=t, ld_x=K + 1, ld_w=K + 1, ld_out=N, ld_dx=K, ld_dw=K, workspace=P,
+                  workspace_bytes=1 << 62)
+        for query in (lambda: L.sc_linear_workspace_bytes(_linear(**kw), P, P),
+                      lambda: L.sc_linear_backward_workspace_bytes(_linear(**kw), P, P, P)):
+            with pytest.raises(L.ScError) as e:
+                query()
+            assert e.value.code == L.SC_ERR_ARG and "2^56" in str(e.value)
+        assert lib.sc_linear(ctypes.byref(_linear(**kw)), P, P, P, P, P, P, None, None) == L.SC_ERR_ARG
+        assert lib.sc_linear_backward(ctypes.byref(_linear(**kw)), P, P, P, P, P, P, P, None, None) == L.SC_ERR_ARG
