@@ -262,6 +262,8 @@ class _On:
         self.dev = torch.cuda.device(device)
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=device)
+        elif stream is not None and stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
         self.st = torch.cuda.stream(stream) if stream is not None else None
 
     def __enter__(self):

@@ -1,9 +1,12 @@
 """More host-side checks of the floating-point layers that need no GPU."""
 import ctypes
+from types import SimpleNamespace
 
 import pytest
+import torch
 
 from mixed_precision_vit_b200 import _lib as L
+from mixed_precision_vit_b200 import sc
 
 P = 4096  # an aligned address that no accepted call here ever reaches
 
@@ -78,3 +81,9 @@ def test_sizes_that_no_byte_count_holds_are_refused(lib, M, N, K):
             assert e.value.code == L.SC_ERR_ARG and "2^56" in str(e.value)
         assert lib.sc_linear(ctypes.byref(_linear(**kw)), P, P, P, P, P, P, None, None) == L.SC_ERR_ARG
         assert lib.sc_linear_backward(ctypes.byref(_linear(**kw)), P, P, P, P, P, P, P, None, None) == L.SC_ERR_ARG
+
+
+def test_a_stream_of_another_device_is_refused():
+    """It would become current, and its device with it, and the work would go elsewhere."""
+    with pytest.raises(ValueError, match="cuda:1"):
+        sc._On(torch.device("cuda", 0), SimpleNamespace(device=torch.device("cuda", 1)))
