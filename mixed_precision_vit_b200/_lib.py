@@ -298,31 +298,8 @@ def sc_selftest_wait_limit(dev_status, limit_cycles, stream=None):
     _check(load().sc_selftest_wait_limit(_ptr(dev_status), int(limit_cycles), _stream(stream)))
 
 
-def sc_layer_norm(desc: ScNormDesc, x, weight, bias, y, mean, rstd, stream=None):
-    _check(load().sc_layer_norm(ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(bias), _ptr(y),
-                                _ptr(mean), _ptr(rstd), _stream(stream)))
-
-
-def sc_layer_norm_backward(desc: ScNormDesc, dy, x, weight, mean, rstd, dx_add, dx, dweight, dbias,
-                           stream=None):
-    _check(load().sc_layer_norm_backward(ctypes.byref(desc), _ptr(dy), _ptr(x), _ptr(weight),
-                                         _ptr(mean), _ptr(rstd), _ptr(dx_add), _ptr(dx),
-                                         _ptr(dweight), _ptr(dbias), _stream(stream)))
-
-
 def sc_layer_norm_workspace_bytes(desc: ScNormDesc) -> int:
     return check_bytes(load().sc_layer_norm_workspace_bytes(ctypes.byref(desc)))
-
-
-def sc_linear(desc: ScLinearDesc, x, w, bias, residual, out, pre, dev_status, stream=None):
-    _check(load().sc_linear(ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(bias), _ptr(residual),
-                            _ptr(out), _ptr(pre), _ptr(dev_status), _stream(stream)))
-
-
-def sc_linear_backward(desc: ScLinearDesc, dout, x, w, pre, dx, dw, dbias, dev_status, stream=None):
-    _check(load().sc_linear_backward(ctypes.byref(desc), _ptr(dout), _ptr(x), _ptr(w), _ptr(pre),
-                                     _ptr(dx), _ptr(dw), _ptr(dbias), _ptr(dev_status),
-                                     _stream(stream)))
 
 
 def sc_selftest_linear_wait_limit(desc: ScLinearDesc, x, w, out, pre, limit_cycles, dev_status, stream=None):
