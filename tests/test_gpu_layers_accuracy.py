@@ -122,3 +122,55 @@ def test_long_contractions_with_16_bit_results(M, N, t):
     x, w = rnd(g, M, K, dtype=t), rnd(g, N, K, dtype=t, scale=K ** -0.5)
     check_linear(x, w, rnd(g, N), rnd(g, M, N, dtype=t), "gelu", want_pre=True)
     check_linear(x, w)
+
+
+# tiles of CTA pairs, of single CTAs, and contractions shared by a cluster
+KERNELS = [(4112, 1024), (1300, 1290), (257, 384), (1, 40)]
+
+
+@pytest.mark.parametrize("t", [BF16, F16, F32])
+@pytest.mark.parametrize("M,N", KERNELS)
+def test_long_sums_of_fp32_results_do_not_drift(M, N, t):
+    """65536 products of one sign.  As above, at most 2^-22 of the sum so far is cut at every 16
+    products: 32.5 * 2^-22 in a chunk of 1024, 16.5 * 2^-22 in one of 512 (fp32 operands, whose
+    left-out products add 4 u); 64 or 128 chunks, or a cluster's parts of them, are added with
+    half a u each on average and a u at most.  In one accumulation the cuts come to 2^-13."""
+    g = gen(54)
+    K = 65536
+    x, w = pos(g, M, K, dtype=t), pos(g, N, K, dtype=t)
+    y = sc.linear(x, w, out_dtype=F32)[0]
+    m, n = slice(0, M, M // 64 + 1), slice(0, N, N // 64 + 1)
+    ref = x[m].double() @ w[n].double().t()
+    cuts = 16.5 * 2.0 ** -22 + (128 + 4) * U if t == F32 else 32.5 * 2.0 ** -22 + 64 * U
+    close(y[m, n], ref, cuts * ref, "out")
+
+
+def parts(g, shape, n):
+    """fp32 values of n bf16 parts, steps of 2^-9 apart, each -1, 0 or 1 of its step; the leading
+    parts of neighbours in the last axis are equal."""
+    v = [torch.randint(-1, 2, shape, device="cuda", generator=g).double() * 2.0 ** (-9 * i) for i in range(n)]
+    v[0][..., 1::2] = v[0][..., ::2]
+    return sum(v).float()
+
+
+@pytest.mark.parametrize("nx,nw", [(3, 1), (1, 3), (2, 2)])
+@pytest.mark.parametrize("M,N", KERNELS)
+def test_every_part_of_fp32_operands_counts(M, N, nx, nw):
+    """Sums that no rounding touches: the products are multiples of 2^-18; the leading parts' run in
+    pairs of opposite signs, so that their sums stay below 2^6, and the others' stay below
+    2048 * 2^-8.  Both fit 24 bits together, so the result is exact, unless a part or one of the
+    six products is left out."""
+    g = gen(55)
+    K = 2048
+    x, w = parts(g, (M, K), nx), parts(g, (N, K), nw)
+    sign = torch.ones(K, device="cuda")
+    sign[1::2] = -1
+    w = w * sign
+    y = sc.linear(x, w)[0]
+    assert torch.equal(y.double(), x.double() @ w.double().t())
+    # the same sums as an input gradient (w^T in place of w) and as a weight gradient
+    dx = sc.linear_backward(x, torch.zeros(M, N, device="cuda"), w.t().contiguous(), want_dw=False, want_db=False)[0]
+    assert torch.equal(dx, y)
+    dw = sc.linear_backward(x.t().contiguous(), w.t().contiguous(), torch.zeros(M, N, device="cuda"), want_dx=False,
+                            want_db=False)[1]
+    assert torch.equal(dw, y)
