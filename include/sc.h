@@ -492,7 +492,8 @@ typedef struct sc_norm_desc {
  *     mu = mean_j x_j,   r = 1 / sqrt(mean_j (x_j - mu)^2 + eps),
  *     y_j = (x_j - mu) r weight_j + bias_j
  * with every sum in fp32 (the variance about the mean, in a second pass over
- * the row on chip) and one rounding to y_type.
+ * the row on chip, which also finds the mean's own rounding, so that rows that
+ * vary little about a large mean keep their accuracy) and one rounding to y_type.
  *   weight, bias  (device, nullable: 1 and 0) [cols]
  *   y             (device) out; may be x itself (same type and stride)
  *   mean, rstd    (device, nullable) fp32 [rows] out: mu and r, for the backward

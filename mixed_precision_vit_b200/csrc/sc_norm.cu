@@ -2,6 +2,12 @@
 //
 // Forward, per row of D values:   mu = sum x / D,  v = sum (x - mu)^2 / D,
 // r = 1 / sqrt(v + eps),  y = (x - mu) r w + b.
+// The mean m of fp32 values is off by the roundings of their sum, |mu - m| up to
+// 2^-20 |mu|, which is more than r bears where a row varies little about a large
+// mean.  With c = x - m (exact there) and t = sum c / D the rest of the mean, v =
+// sum c^2 / D - t^2 and y = (c - t) r w + b: one more sum beside that of the
+// squares (65792 x 1024 fp32 -> bf16 65.0 -> 66.8 us).  16-bit values that lie
+// close together add up exactly in 24 bits, so their mean needs no rest.
 // Backward, with h = (x - mu) r, g = dy w, s1 = sum_j g, s2 = sum_j g h:
 //   dx = r (g - (s1 + h s2) / D) [+ dx_add],
 //   dw_j = sum_i dy_ij h_ij,  db_j = sum_i dy_ij.
@@ -50,18 +56,56 @@ __device__ __forceinline__ float row_sum(float v, float *red) {
     return v;
 }
 
+// Two sums at once (BOTH; else of b alone); `red` holds one float2 per warp.
+template <int T, bool BOTH>
+__device__ __forceinline__ float2 row_sum2(float a, float b, float2 *red) {
+    float2 v = make_float2(BOTH ? warp_sum(a) : 0.f, warp_sum(b));
+    if constexpr (T > 32) {
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = red[0];
+#pragma unroll
+        for (int i = 1; i < T / 32; ++i) {
+            if (BOTH) v.x += red[i].x;
+            v.y += red[i].y;
+        }
+    }
+    return v;
+}
+
+// s / D from inv = 1 / D with one step of correction, so that a constant row gives
+// its value (4099 x 997 takes a third longer with divisions instead).
+__device__ __forceinline__ float divided(float s, float D, float inv) {
+    const float q = s * inv;
+    return fmaf(fmaf(-q, D, s), inv, q);
+}
+
+// The rest t of a row's mean and r, from the sums of c and c^2 (c = x - m).
+struct Spread {
+    float rest, rstd;
+};
+template <bool REST>
+__device__ __forceinline__ Spread spread(float s1, float s2, float D, float inv, float eps) {
+    const float t = REST ? divided(s1, D, inv) : 0.f;
+    if (REST) s2 = fmaxf(fmaf(-s1, t, s2), 0.f);
+    return {t, 1.f / sqrtf(s2 * inv + eps)};
+}
+
 // T threads per row, each holding NC chunks of E columns (chunk c of thread t
-// starts at column (c T + t) E), so D <= T NC E; rows and D are aligned for E.
+// starts at column (c T + t) E), so D <= T NC E; rows and D are aligned for E,
+// which is even: the arithmetic runs on two values at a time.
 template <typename TX, typename TY, int E, int NC, int T>
 __global__ void __launch_bounds__(T < 128 ? 128 : T) ln_fwd_kernel(const NormArgs p) {
+    constexpr bool REST = sizeof(TX) == 4;
     constexpr int RPB = T < 128 ? 128 / T : 1;
-    __shared__ float red[2][T / 32];
+    __shared__ float red[T / 32];
+    __shared__ float2 red2[T / 32];
     const int t = threadIdx.x % T;
     const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / T;
     if (row >= p.rows) return;  // whole warps (T = 32) only
     const TX *x = static_cast<const TX *>(p.x) + row * p.ld_x;
     float v[NC][E];
-    float s = 0.f;
+    float2 s = make_float2(0.f, 0.f);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
         const int64_t col = (int64_t)(c * T + t) * E;
@@ -72,19 +116,28 @@ __global__ void __launch_bounds__(T < 128 ? 128 : T) ln_fwd_kernel(const NormArg
             for (int e = 0; e < E; ++e) v[c][e] = 0.f;
         }
 #pragma unroll
-        for (int e = 0; e < E; ++e) s += v[c][e];
+        for (int e = 0; e < E; e += 2) s = add2(s, make_float2(v[c][e], v[c][e + 1]));
     }
     const float inv = 1.f / (float)p.cols;
-    const float mu = row_sum<T>(s, red[0]) * inv;
-    s = 0.f;
+    const float mu = divided(row_sum<T>(s.x + s.y, red), (float)p.cols, inv);
+    const float2 m2 = make_float2(-mu, -mu);
+    float2 s2 = s = make_float2(0.f, 0.f);
 #pragma unroll
     for (int c = 0; c < NC; ++c)
         if ((int64_t)(c * T + t) * E < p.cols)
 #pragma unroll
-            for (int e = 0; e < E; ++e) s += (v[c][e] - mu) * (v[c][e] - mu);
-    const float r = 1.f / sqrtf(row_sum<T>(s, red[1]) * inv + p.eps);
+            for (int e = 0; e < E; e += 2) {
+                const float2 d = add2(make_float2(v[c][e], v[c][e + 1]), m2);
+                if (REST) s = add2(s, d);
+                s2 = fma2(d, d, s2);
+                v[c][e] = d.x;
+                v[c][e + 1] = d.y;
+            }
+    const float2 sums = row_sum2<T, REST>(s.x + s.y, s2.x + s2.y, red2);
+    const Spread q = spread<REST>(sums.x, sums.y, (float)p.cols, inv, p.eps);
+    const float r = q.rstd;
     if (t == 0) {
-        if (p.mean) p.mean[row] = mu;
+        if (p.mean) p.mean[row] = mu + q.rest;
         if (p.rstd) p.rstd[row] = r;
     }
     TY *y = static_cast<TY *>(p.y) + row * p.ld_y;
@@ -101,7 +154,13 @@ __global__ void __launch_bounds__(T < 128 ? 128 : T) ln_fwd_kernel(const NormArg
         if (p.w) load_any<E>(p.w, p.w_type, col, w);
         if (p.b) load_any<E>(p.b, p.w_type, col, b);
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[c][e] = (v[c][e] - mu) * r * w[e] + b[e];
+        for (int e = 0; e < E; e += 2) {
+            float2 d = make_float2(v[c][e], v[c][e + 1]);
+            if (REST) d = add2(d, make_float2(-q.rest, -q.rest));
+            const float2 o = fma2(mul2(d, make_float2(r, r)), make_float2(w[e], w[e + 1]), make_float2(b[e], b[e + 1]));
+            v[c][e] = o.x;
+            v[c][e + 1] = o.y;
+        }
         store_vec<TY, E>(y + col, v[c]);
     }
 }
@@ -111,7 +170,9 @@ __global__ void __launch_bounds__(T < 128 ? 128 : T) ln_fwd_kernel(const NormArg
 template <typename TX, typename TY, int E>
 __global__ void __launch_bounds__(512) ln_fwd_wide_kernel(const NormArgs p) {
     constexpr int T = 512;
-    __shared__ float red[2][T / 32];
+    constexpr bool REST = sizeof(TX) == 4;
+    __shared__ float red[T / 32];
+    __shared__ float2 red2[T / 32];
     const int64_t row = blockIdx.x;
     const TX *x = static_cast<const TX *>(p.x) + row * p.ld_x;
     TY *y = static_cast<TY *>(p.y) + row * p.ld_y;
@@ -123,16 +184,22 @@ __global__ void __launch_bounds__(512) ln_fwd_wide_kernel(const NormArgs p) {
         for (int e = 0; e < E; ++e) s += v[e];
     }
     const float inv = 1.f / (float)p.cols;
-    const float mu = row_sum<T>(s, red[0]) * inv;
+    const float mu = divided(row_sum<T>(s, red), (float)p.cols, inv);
+    float s2 = 0.f;
     s = 0.f;
     for (int64_t col = (int64_t)threadIdx.x * E; col < p.cols; col += T * E) {
         load_vec<TX, E>(x + col, v);
 #pragma unroll
-        for (int e = 0; e < E; ++e) s += (v[e] - mu) * (v[e] - mu);
+        for (int e = 0; e < E; ++e) {
+            if (REST) s += v[e] - mu;
+            s2 += (v[e] - mu) * (v[e] - mu);
+        }
     }
-    const float r = 1.f / sqrtf(row_sum<T>(s, red[1]) * inv + p.eps);
+    const float2 sums = row_sum2<T, REST>(s, s2, red2);
+    const Spread q = spread<REST>(sums.x, sums.y, (float)p.cols, inv, p.eps);
+    const float r = q.rstd;
     if (threadIdx.x == 0) {
-        if (p.mean) p.mean[row] = mu;
+        if (p.mean) p.mean[row] = mu + q.rest;
         if (p.rstd) p.rstd[row] = r;
     }
     for (int64_t col = (int64_t)threadIdx.x * E; col < p.cols; col += T * E) {
@@ -146,7 +213,7 @@ __global__ void __launch_bounds__(512) ln_fwd_wide_kernel(const NormArgs p) {
         if (p.w) load_any<E>(p.w, p.w_type, col, w);
         if (p.b) load_any<E>(p.b, p.w_type, col, b);
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = (v[e] - mu) * r * w[e] + b[e];
+        for (int e = 0; e < E; ++e) v[e] = (v[e] - mu - q.rest) * r * w[e] + b[e];
         store_vec<TY, E>(y + col, v);
     }
 }
@@ -264,6 +331,7 @@ __device__ __forceinline__ void group_sum2(float &a, float &b, float (*red)[2], 
 template <typename TX, typename TY, int E, int NC, int T, int NT>
 __global__ void __launch_bounds__(NT) ln_fwd_any_kernel(const NormArgs p) {
     constexpr int G = NT / T;
+    constexpr bool REST = sizeof(TX) == 4;
     __shared__ float red[2][NT / 32][2];
     const int t = threadIdx.x % T, g = threadIdx.x / T, D = (int)p.cols;
     const int64_t first = (int64_t)blockIdx.x * G + g, step = (int64_t)gridDim.x * G;
@@ -297,27 +365,32 @@ __global__ void __launch_bounds__(NT) ln_fwd_any_kernel(const NormArgs p) {
 #pragma unroll
             for (int e = 0; e < E; ++e) s += v[c][e];
         group_sum2<T, NT>(s, unused, red[0], g);
-        const float mu = s * inv;
+        const float mu = divided(s, (float)D, inv);
+        float s2 = 0.f;
         s = 0.f;
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 const int col = (c * T + t) * E - shift + e;
-                const float d = v[c][e] - mu;
-                if (col >= 0 && col < D) s += d * d;
+                v[c][e] -= mu;
+                if (col >= 0 && col < D) {
+                    if (REST) s += v[c][e];
+                    s2 += v[c][e] * v[c][e];
+                }
             }
-        group_sum2<T, NT>(s, unused, red[1], g);
-        const float r = 1.f / sqrtf(s * inv + p.eps);
+        group_sum2<T, NT>(s, s2, red[1], g);
+        const Spread q = spread<REST>(s, s2, (float)D, inv, p.eps);
+        const float r = q.rstd;
         if (t == 0) {
-            if (p.mean) p.mean[row] = mu;
+            if (p.mean) p.mean[row] = mu + q.rest;
             if (p.rstd) p.rstd[row] = r;
         }
         TY *y = static_cast<TY *>(p.y) + row * p.ld_y;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) v[c][e] = (v[c][e] - mu) * r * w[c][e] + b[c][e];
+            for (int e = 0; e < E; ++e) v[c][e] = (v[c][e] - q.rest) * r * w[c][e] + b[c][e];
             store_cols<TY, E>(y, (c * T + t) * E - shift, D, v[c]);
         }
     }
