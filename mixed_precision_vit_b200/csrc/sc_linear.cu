@@ -270,6 +270,16 @@ struct Scratch {
     }
 };
 
+// A matrix that the product reads where it is.  One row's stride means nothing,
+// so a tensor map, which takes strides below 2^40 bytes, gets another.
+GemmOperand placed(const void *p, int64_t rows, int64_t cols, int64_t ld) {
+    GemmOperand o = {};
+    o.p = p;
+    o.ld = rows > 1 ? ld : round_up(cols, 8);
+    o.planes = 1;
+    return o;
+}
+
 GemmOperand copied(void *p, int64_t rows, int64_t cols, int type) {
     GemmOperand o = {};
     o.p = p;
@@ -284,9 +294,7 @@ GemmOperand operand(const void *p, int64_t rows, int64_t cols, int64_t ld, int t
                     Passes &passes) {
     GemmOperand o = {};
     if (in_place(p, ld, type)) {
-        o.p = p;
-        o.ld = ld;
-        o.planes = 1;
+        o = placed(p, rows, cols, ld);
     } else {
         o = copied(ws.take(copy_bytes(rows, cols, type)), rows, cols, type);
         PassJob j = {};
@@ -498,9 +506,7 @@ extern "C" int sc_linear_backward(const sc_linear_desc *d, const void *dout, con
     if (dbias) p.part = static_cast<float *>(ws.take(part_bytes(*d)));
     GemmOperand dz = {};
     if (dz_in_place(*d, dout)) {
-        dz.p = dout;
-        dz.ld = d->ld_out;
-        dz.planes = 1;
+        dz = placed(dout, d->M, d->N, d->ld_out);
     } else if (dx || dw) {
         dz = copied(ws.take(copy_bytes(d->M, d->N, d->type)), d->M, d->N, d->type);
         p.dst = const_cast<void *>(dz.p);

@@ -55,3 +55,26 @@ def test_a_part_of_the_gradients_takes_less_memory():
     assert peak(want_db=True) < small
     assert peak(want_dx=True) < dz + ws + 4 * x.numel() + small
     assert peak(want_dw=True) < dz + xs + 4 * w.numel() + small
+
+
+@pytest.mark.parametrize("t", [BF16, F32])
+def test_a_single_row_has_any_stride(t):
+    """A stride of 2^45 elements between rows that do not exist."""
+    g = gen(72)
+    N, K, far = 64, 128, 1 << 45
+    x, dout, w = rnd(g, 1, K, dtype=t), rnd(g, 1, N, dtype=t), rnd(g, N, K, dtype=t)
+    stream = torch.cuda.current_stream().cuda_stream
+    out, dx, dw = torch.empty_like(dout), torch.empty_like(x), torch.empty_like(w)
+    k = sc._TYPES[t]
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    d = L.ScLinearDesc(1, N, K, far, K, far, 0, 0, far, K, k, k, 0, k, 0, ws.data_ptr(), ws.numel())
+    L.check(L.lib().sc_linear(d, *(L._ptr(p) for p in (x, w, None, None, out, None)), None, stream))
+    assert torch.equal(out, sc.linear(x, w)[0])
+    L.check(L.lib().sc_linear_backward(d, *(L._ptr(p) for p in (dout, x, w, None, dx, dw, None)), None, stream))
+    ref = sc.linear_backward(dout, x, w, want_db=False)
+    assert torch.equal(dx, ref[0]) and torch.equal(dw, ref[1])
+    # w of one row, and its gradient's
+    one, col = w[:1].contiguous(), torch.empty(1, 1, dtype=t, device="cuda")
+    d = L.ScLinearDesc(1, 1, K, far, far, far, 0, 0, far, far, k, k, 0, k, 0, ws.data_ptr(), ws.numel())
+    L.check(L.lib().sc_linear(d, *(L._ptr(p) for p in (x, one, None, None, col, None)), None, stream))
+    assert torch.equal(col, sc.linear(x, one)[0])
