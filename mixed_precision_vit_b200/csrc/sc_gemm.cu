@@ -129,15 +129,18 @@ struct Shape {
 // The tile shape with the least estimated time.  Measured (us, bf16): a stage
 // of 64 indexes costs 0.30 in a pair's 256 x 256 tile and 0.24 in a CTA's 128 x
 // 128 tile or less (there the issuing threads, not the products, set the pace);
-// a launch 6.0 or 5.0 besides; parts of a shared tile cost their exchange,
-// 0.005 per column and part.  So 4112 x 1024 x 4096 takes 25.5 in pairs
+// a launch 6.0 or 5.0 besides; a shared tile costs 0.008 per column for its
+// epilogue and 0.005 per column and part for the exchange.  So 4112 x 1024 x 4096 takes 25.5 in pairs
 // (68 tiles, one round) and 37.2 in single CTAs (264 tiles, two rounds); 2056 x
 // 1024 x 1024 takes 10.6 and 8.5; 257 x 1024 x 4096 takes 13.0 in 4 parts of
 // 128 columns and 28 unshared.  A step of fp32 operands (three stages, six
 // products) costs 1.75 in a pair, 1.2 in a CTA alone, 1.1 and 1.0 in parts of 128
-// and 64 columns: 257 x 1024 x 1024 takes 17.2 in 4 parts of 128, 18.2 in 2 of 64,
-// 28.4 unshared, all with their operands' pass; 4112 x 1024 x 1024 49.2 in pairs
-// and 56.4 in single CTAs.
+// and 64 columns: 257 x 1024 x 1024 takes 17.0 in 4 parts of 128, 17.5 in 2 of 64,
+// 28.4 unshared, all with their operands' pass; 4112 x 1024 x 1024 48.5 in pairs
+// and 56.4 in single CTAs.  Of 20 problems (1 to 514 rows, 512 to 4096 columns and
+// indexes, fp32 and bf16) with every shape timed, the rule takes the fastest or one
+// within 3 % in 18; 257 x 1024 x 4096 bf16 takes 14.3 in 5 parts, 13.0 in 4; 1 x 1000
+// x 1024 fp32 11.1 in 6 of 64 columns, 10.5 in 8 of 128.
 Shape choose(int64_t M, int64_t N, int n_k, int planes) {
     const int sms = sm_count();
     auto rounds = [](int64_t tiles, int units) { return (double)div_up(tiles, units < 1 ? 1 : units); };
@@ -158,9 +161,10 @@ Shape choose(int64_t M, int64_t N, int n_k, int planes) {
         // each part of a shared tile takes two stages or more
         for (int parts = 2; parts <= MAX_PARTS && 2 * parts <= planes * n_k && parts <= n_k && tiles * parts <= sms;
              ++parts)
-            // One cluster fewer than fit: a device full of them does not pay
-            // (257 x 1024 x 1024 fp32 in 24 clusters of 5 CTAs, all that fit:
-            // 19.0, of 4 17.2; 16-bit operands alike in both).
+            // One cluster fewer than fit: a device full of them, or more, does
+            // not pay (257 x 1024 x 1024 fp32 in 24 clusters of 5 CTAs: 18.6, of 6
+            // 25.7, of 4 16.9; 257 x 768 x 768 in 18 of 6 15.5, of 4 14.2; 257 x
+            // 1024 x 1024 bf16 of 5 12.1, of 4 10.1).
             if (tiles < split_clusters(parts))
                 consider({1, bn, parts}, 5.0 + 0.008 * bn + 0.005 * bn * parts + step * (double)div_up(n_k, parts));
     }

@@ -12,7 +12,7 @@
 // significand, |x2| <= 2^-8 |x|, |x3| <= 2^-16 |x|.  Of the nine products the
 // three below 2^-24 |x w| are left out.  The same part of both operands makes a
 // stage, and the other six products run as their stages arrive, so that 64
-// indexes take three stages.  (257 x 1024 x 1024 with its pass takes 17.3 us, 2056
+// indexes take three stages.  (257 x 1024 x 1024 with its pass takes 17.1 us, 2056
 // x 1024 x 1024 32; as six products over the parts one after the other, 19.4 and
 // 38; with the six operand tiles as stages of their own 21.7 and 38: every stage
 // costs the issuing threads its waits.)
@@ -20,14 +20,15 @@
 // The tensor cores cut an fp32 sum where fp32 arithmetic rounds, so a long sum
 // drifts towards zero by about 2^-25 of itself per 16 indexes.  Where the
 // result keeps fp32, an accumulator therefore takes CHUNK steps at most, and
-// the epilogue warps add the chunks in registers (32896 x 1024 x 4096: off by
-// 9.2e-7 of the result's norm, 4.0e-6 in one accumulation; CHUNK / 2 would make
-// it 4.7e-7 in 243 us instead of 230).  A 16-bit result's rounding hides the
+// the epilogue warps add the chunks in registers (32896 x 1024 x 4096 with an
+// fp32 residual: off by 1.0e-6 of the result's norm, 4.0e-6 in one accumulation;
+// CHUNK / 2 would make it 4.8e-7 in 225 us instead of 212).  A 16-bit result's rounding hides the
 // drift of LONG_16 steps (2^-15, half a step of fp16 is 2^-11); longer sums
-// are added up in chunks too.  fp32 operands keep the five small
+// are added up in chunks too (2048 x 2048 x 16384 in one accumulation 91.0 us,
+// 2048 x 2048 x 16448 in chunks 92.6).  fp32 operands keep the five small
 // products, below 2^-8 of the result, in an accumulator of their own, so that
 // only the leading product's drift counts, and take CHUNK_F32 steps (8: off by
-// 4.7e-7 where 16 are off by 1.0e-6; 4112 x 4096 x 1024 takes 164 us, 160 with
+// 4.7e-7 where 16 are off by 1.0e-6; 4112 x 4096 x 1024 takes 157 us, 154 with
 // 16; a plain fp32 product is off by 5.7e-7).
 //
 // Kernels (one template):
@@ -41,11 +42,13 @@
 // Warp 0 issues the copies, warp 1 the products, warp 3 finishes column sums of
 // an earlier pass if the caller has any, warps 4 to 11 are the epilogue.
 //
-// Measured (us, one B200, inputs larger than L2 in turn): 8192^3 bf16 692
-// (cuBLAS 689); 4112 x 4096 x 1024 26 plain (cuBLAS 27), 36 with gelu and the
-// pre-activation kept, where the epilogue sets the pace (tensor pipe 55 % busy);
-// 32896 x 1024 x 4096 with an fp32 residual and result 216 (tensor pipe 79 %;
-// cuBLAS 195 without either).
+// Measured (us, one B200, a replayed graph over two or three sets of inputs after a
+// second's rest): 8192^3 bf16 690 (cuBLAS 654); 4112 x 4096 x 1024 30 plain
+// (cuBLAS 29), 40 with gelu and the pre-activation kept, where the epilogue sets
+// the pace (tensor pipe 51 % busy); 32896 x 1024 x 4096 178 (cuBLAS 179), 211 with
+// an fp32 residual and result (tensor pipe 77 %).  Products that run for longer
+// meet the power limit: the last one takes 247 us replayed and 259 called for 1.5 s,
+// at 1180 and 1120 MHz.
 // All waits are bounded, as in the count engine.  A CTA (a pair, a cluster that
 // shares a tile) whose wait expires waits for its own copies and products,
 // writes NaN over its tiles, records SC_DEV_WAIT_LIMIT, frees tensor memory and

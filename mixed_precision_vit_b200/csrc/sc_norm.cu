@@ -12,10 +12,10 @@
 //   dx = r (g - (s1 + h s2) / D) [+ dx_add],
 //   dw_j = sum_i dy_ij h_ij,  db_j = sum_i dy_ij.
 // Both are bound by device memory: a row is read once and held in registers.
-// Of the copy's 6.45 TB/s: 65792 x 1024 fp32 -> bf16 65 us (96 %), the same
-// bf16 -> bf16 53 us (78 %: weight and bias, read per row from L1, are twice its
-// bytes); backward of 32896 x 1024 fp32 71 us (88 %).  Small calls are launches:
-// 257 x 1024 3.2 us.
+// Of the copy's 6.45 TB/s: 65792 x 1024 fp32 -> bf16 67 us (93 %), the same
+// bf16 -> bf16 55 us (76 %: weight and bias, read per row from L1, are twice its
+// bytes); backward of 32896 x 1024 fp32 72 us (87 %).  Small calls are launches:
+// 257 x 1024 3.0 us.
 #include <initializer_list>
 #include <type_traits>
 
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(NT) ln_fwd_any_kernel(const NormArgs p) {
 // columns; the block adds its groups' sums up in shared memory and writes one
 // partial row of each (summed over blocks by finish_columns_kernel).  One block
 // of 512 threads per SM keeps the partial rows few (444 blocks of 128 threads
-// took 19 us for 4112 x 1024 bf16 with dx_add, these 13.7); its groups' rows in
+// took 19 us for 4112 x 1024 bf16 with dx_add, these 12.3); its groups' rows in
 // flight hide the memory's latency.
 template <typename TX, typename TY, int E, int NC, int T, int NT>
 __global__ void __launch_bounds__(NT, 1) ln_bwd_kernel(const NormArgs p) {

@@ -185,7 +185,12 @@ def matmul(a_lv, a_s, b_lv, b_s, rung, perm, offs, table: ScTable, *, op=L.SC_OP
 # ---- floating-point layers of a transformer block ---------------------------------
 # Matrices are given as [..., columns] tensors whose rows lie one fixed stride apart
 # (contiguous, or a view such as x[:, 0] or x[:, :n]); anything else is refused rather
-# than copied.  Work goes to `stream`, or to torch's current stream of the tensors' device.
+# than copied.  Work goes to `stream`, or to torch's current stream of the tensors' device;
+# results belong to that stream, and tensors of other streams follow torch's usual rules
+# (wait for what writes them, record_stream before they are freed).
+# The layers are outside of torch's autograd: a result never requires a gradient, whatever its
+# inputs do, and loss.backward() stops there without an error.  The backward calls give the
+# gradients; a torch.autograd.Function of the caller's can join the two.
 
 _TYPES = {torch.float32: L.SC_F32, torch.bfloat16: L.SC_BF16, torch.float16: L.SC_F16}
 ACTIVATIONS = {"none": L.SC_ACT_NONE, "relu": L.SC_ACT_RELU, "gelu": L.SC_ACT_GELU,
@@ -322,7 +327,8 @@ def layer_norm(x: torch.Tensor, weight=None, bias=None, eps: float = 1e-6, *, ou
     weight, bias: [D] of one type, or None.  y has out_dtype (x's by default; fp32 may
     become 16 bits and back, e.g. fp32 for quantize() after a bf16 block).  mean and rstd
     (fp32, x.shape[:-1]) are returned with want_stats, for layer_norm_backward, and are
-    None otherwise.  out: the tensor to write, which may be x itself (same type)."""
+    None otherwise.  out: the tensor to write, which may be x itself (same type).
+    Gradients: layer_norm_backward; autograd does not see this call."""
     rows, D, ld = _matrix(x, "x")
     dev = x.get_device()
     if stream is not None or dev != torch.cuda.current_device():
@@ -412,6 +418,7 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias=None, residual=None, act="none
     out_dtype, which is x's type (default) or float32.  act: a key of ACTIVATIONS.  pre
     is x w^T + bias in x's type with want_pre (what linear_backward needs for an
     activation), else None.  out: the tensor to write, which may be the residual.
+    Gradients: linear_backward; autograd does not see this call.
     workspace: device scratch of sc_linear_workspace_bytes, allocated when None.
     dev_status: int32 tensor that receives SC_DEV_WAIT_LIMIT if an internal wait gave up;
     the blocks of out and pre that it concerns are then NaN, with or without it."""
@@ -456,7 +463,8 @@ def linear_backward(dout: torch.Tensor, x: torch.Tensor, w: torch.Tensor, pre=No
     """Gradients of linear: (dx, dw, db), each None where it is not wanted.
 
     dout [..., N] of x's type or float32; pre as linear returned it (needed with an
-    activation).  dx has x's type, dw and db grad_dtype (w's type by default).  The
+    activation).  With 16-bit operands dout act'(pre) is rounded to their type for the two
+    products.  dx has x's type, dw and db grad_dtype (w's type by default).  The
     residual's gradient is dout itself.  workspace: device scratch of
     sc_linear_backward_workspace_bytes, allocated when None."""
     M, K, ld_x = _matrix(x, "x")
