@@ -20,16 +20,18 @@
 // The tensor cores cut an fp32 sum where fp32 arithmetic rounds, so a long sum
 // drifts towards zero by about 2^-25 of itself per 16 indexes.  Where the
 // result keeps fp32, an accumulator therefore takes CHUNK steps at most, and
-// the epilogue warps add the chunks in registers (32896 x 1024 x 4096 with an
-// fp32 residual: off by 1.0e-6 of the result's norm, 4.0e-6 in one accumulation;
-// CHUNK / 2 would make it 4.8e-7 in 225 us instead of 212).  A 16-bit result's rounding hides the
+// the epilogue warps add the chunks in registers.  (32896 x 1024 x 4096 with an
+// fp32 residual: off by 4.7e-7 of the result's norm in 239 us; 9.9e-7 in 228 with
+// chunks of 16, 4.0e-6 in one accumulation; a plain fp32 product is off by 6.1e-7.
+// 4112 x 4096 x 1024 takes 52 and 51, others alike: what costs time is that two
+// chunks of the next tile are all that runs under a tile's stores.)  A 16-bit result's rounding hides the
 // drift of LONG_16 steps (2^-15, half a step of fp16 is 2^-11); longer sums
 // are added up in chunks too (2048 x 2048 x 16384 in one accumulation 91.0 us,
 // 2048 x 2048 x 16448 in chunks 92.6).  fp32 operands keep the five small
 // products, below 2^-8 of the result, in an accumulator of their own, so that
-// only the leading product's drift counts, and take CHUNK_F32 steps (8: off by
-// 4.7e-7 where 16 are off by 1.0e-6; 4112 x 4096 x 1024 takes 157 us, 154 with
-// 16; a plain fp32 product is off by 5.7e-7).
+// only the leading product's drift counts (off by 4.7e-7 where chunks of 16 are
+// off by 1.0e-6; 4112 x 4096 x 1024 takes 157 us, 154 with 16; a plain fp32 product
+// is off by 5.7e-7).
 //
 // Kernels (one template):
 //   CG = 2  clusters of two CTAs on two SMs, one cta_group::2 MMA of 256 rows x
@@ -73,8 +75,7 @@ constexpr int GEMM_THREADS = (EPI_WARP0 + EPI_WARPS) * 32;
 constexpr int KEEP_REGS = 168;          // registers per thread of a kernel that keeps sums
 constexpr int RING_BYTES = 160 * 1024;  // 5 stages of 32 KB
 constexpr int MAX_RING = 8;
-constexpr int CHUNK = 16;               // steps (1024 indexes) per accumulation of an fp32 result
-constexpr int CHUNK_F32 = 8;            // with fp32 operands
+constexpr int CHUNK = 8;                // steps (512 indexes) per accumulation of an fp32 result
 constexpr int LONG_16 = 256;            // most steps of a 16-bit result in one accumulation
 // Epilogue staging, per warp: 32 rows x 64 columns of fp32, 16-byte quads
 // permuted so that both a lane's row (written) and 8 lanes' row (read) touch

@@ -88,8 +88,8 @@ def pos(g, *shape, dtype, scale=1.0):
 def test_long_sums_of_16_bit_results_do_not_drift(N, K, t):
     """A weight gradient over 262144 rows of one sign, in tiles of either width.  The tensor
     cores cut at every 16 products, below 2^-22 of the sum so far for all of them together:
-    (1 + .. + 64) / 64 * 2^-22 < 2^-16.9 in a chunk of 1024; 256 chunks add up with half of
-    256 u = 2^-17.  In one accumulation the cuts come to about 2^-11."""
+    (1 + .. + 32) / 32 * 2^-22 < 2^-17.9 in a chunk of 512; 512 chunks add up with u (1 + .. +
+    512) / 512 at most = 2^-16.  In one accumulation the cuts come to about 2^-11."""
     g = gen(51)
     M = 262144
     x, dout = pos(g, M, K, dtype=t), pos(g, M, N, dtype=t, scale=0.25)
@@ -97,7 +97,7 @@ def test_long_sums_of_16_bit_results_do_not_drift(N, K, t):
     dw = sc.linear_backward(dout, x, w, want_dx=False, want_db=False)[1]
     n, k = slice(0, N, N // 64 + 1), slice(0, K, K // 64 + 1)
     ref = dout[:, n].double().t() @ x[:, k].double()
-    close(dw[n, k], ref, 2.0 ** -15.9 * ref, "dw")
+    close(dw[n, k], ref, (2.0 ** -17.9 + 2.0 ** -16) * ref, "dw")
 
 
 @pytest.mark.parametrize("gt", [F16, BF16])
@@ -132,17 +132,31 @@ KERNELS = [(4112, 1024), (1300, 1290), (257, 384), (1, 40)]
 @pytest.mark.parametrize("M,N", KERNELS)
 def test_long_sums_of_fp32_results_do_not_drift(M, N, t):
     """65536 products of one sign.  As above, at most 2^-22 of the sum so far is cut at every 16
-    products: 32.5 * 2^-22 in a chunk of 1024, 16.5 * 2^-22 in one of 512 (fp32 operands, whose
-    left-out products add 4 u); 64 or 128 chunks, or a cluster's parts of them, are added with
-    half a u each on average and a u at most.  In one accumulation the cuts come to 2^-13."""
+    products: 16.5 * 2^-22 in a chunk of 512 (fp32 operands' left-out products add 4 u); 128
+    chunks, or a cluster's parts of them, are added with a u each at most.  In one accumulation
+    the cuts come to 2^-13."""
     g = gen(54)
     K = 65536
     x, w = pos(g, M, K, dtype=t), pos(g, N, K, dtype=t)
     y = sc.linear(x, w, out_dtype=F32)[0]
     m, n = slice(0, M, M // 64 + 1), slice(0, N, N // 64 + 1)
     ref = x[m].double() @ w[n].double().t()
-    cuts = 16.5 * 2.0 ** -22 + (128 + 4) * U if t == F32 else 32.5 * 2.0 ** -22 + 64 * U
-    close(y[m, n], ref, cuts * ref, "out")
+    close(y[m, n], ref, (16.5 * 2.0 ** -22 + (128 + 4 * (t == F32)) * U) * ref, "out")
+
+
+@pytest.mark.parametrize("t", [BF16, F16, F32])
+@pytest.mark.parametrize("at", [0, 1024])
+@pytest.mark.parametrize("M,N", KERNELS)
+def test_what_one_accumulation_can_lose(M, N, t, at):
+    """One product of 2^23 makes the accumulator's last place 1; 16 others together are 15/16, which
+    a cut drops.  So at most the 64 * 15/256 = 3.75 of every one of the 8 steps that share the
+    large product's accumulation are lost.  The other accumulations are exact, and their sums too."""
+    K = 4096
+    x, w = torch.full((M, K), 15 / 16, device="cuda"), torch.full((N, K), 1 / 16, device="cuda")
+    x[:, at], w[:, at] = 4096, 2048
+    y = sc.linear(x.to(t), w.to(t), out_dtype=F32)[0].double()
+    lost = 2.0 ** 23 + (K - 1) * 15 / 256 - y
+    assert (lost >= -1).all() and (lost <= 8 * 3.75 + 1).all(), (lost.min().item(), lost.max().item())
 
 
 def parts(g, shape, n):
