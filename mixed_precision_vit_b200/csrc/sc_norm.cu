@@ -77,17 +77,22 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, float2 *red) {
 // its value (4099 x 997 takes a third longer with divisions instead).
 __device__ __forceinline__ float divided(float s, float D, float inv) {
     const float q = s * inv;
-    return fmaf(fmaf(-q, D, s), inv, q);
+    return isinf(q) ? q : fmaf(fmaf(-q, D, s), inv, q);
 }
 
 // The rest t of a row's mean and r, from the sums of c and c^2 (c = x - m).
 struct Spread {
     float rest, rstd;
+    // an infinite m stays what it is
+    __device__ __forceinline__ float mean(float m) const { return isinf(m) ? m : m + rest; }
 };
 template <bool REST>
 __device__ __forceinline__ Spread spread(float s1, float s2, float D, float inv, float eps) {
     const float t = REST ? divided(s1, D, inv) : 0.f;
-    if (REST) s2 = fmaxf(fmaf(-s1, t, s2), 0.f);
+    if (REST) {
+        s2 = fmaf(-s1, t, s2);
+        if (s2 < 0.f) s2 = 0.f;  // keeps a NaN
+    }
     return {t, 1.f / sqrtf(s2 * inv + eps)};
 }
 
@@ -137,7 +142,7 @@ __global__ void __launch_bounds__(T < 128 ? 128 : T) ln_fwd_kernel(const NormArg
     const Spread q = spread<REST>(sums.x, sums.y, (float)p.cols, inv, p.eps);
     const float r = q.rstd;
     if (t == 0) {
-        if (p.mean) p.mean[row] = mu + q.rest;
+        if (p.mean) p.mean[row] = q.mean(mu);
         if (p.rstd) p.rstd[row] = r;
     }
     TY *y = static_cast<TY *>(p.y) + row * p.ld_y;
@@ -199,7 +204,7 @@ __global__ void __launch_bounds__(512) ln_fwd_wide_kernel(const NormArgs p) {
     const Spread q = spread<REST>(sums.x, sums.y, (float)p.cols, inv, p.eps);
     const float r = q.rstd;
     if (threadIdx.x == 0) {
-        if (p.mean) p.mean[row] = mu + q.rest;
+        if (p.mean) p.mean[row] = q.mean(mu);
         if (p.rstd) p.rstd[row] = r;
     }
     for (int64_t col = (int64_t)threadIdx.x * E; col < p.cols; col += T * E) {
@@ -383,7 +388,7 @@ __global__ void __launch_bounds__(NT) ln_fwd_any_kernel(const NormArgs p) {
         const Spread q = spread<REST>(s, s2, (float)D, inv, p.eps);
         const float r = q.rstd;
         if (t == 0) {
-            if (p.mean) p.mean[row] = mu + q.rest;
+            if (p.mean) p.mean[row] = q.mean(mu);
             if (p.rstd) p.rstd[row] = r;
         }
         TY *y = static_cast<TY *>(p.y) + row * p.ld_y;

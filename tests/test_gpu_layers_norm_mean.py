@@ -43,3 +43,16 @@ def test_rows_about_a_large_mean(D, mean):
     close(y, ref, w.double().abs() * r * (c.abs() + c.abs().mean(-1, keepdim=True)) * (lost + 4 * U) + 2 * U * b.double().abs())
     close(mu, m[:, 0], d * U * c.abs().mean(-1))
     close(rstd, r[:, 0], (lost * r)[:, 0])
+
+
+@pytest.mark.parametrize("t", [F32, BF16])
+@pytest.mark.parametrize("D", [64, 997, 4096, 20000, 16391])
+def test_statistics_of_nonfinite_rows(D, t):
+    x = rnd(gen(83), 5, D, dtype=t)
+    clean = sc.layer_norm(x, want_stats=True)
+    x[1, D // 2], x[3, 0] = float("nan"), float("-inf")
+    got = sc.layer_norm(x, want_stats=True)
+    for a, b in zip(got, clean):
+        assert torch.equal(a[[0, 2, 4]], b[[0, 2, 4]])
+    assert got[0][[1, 3]].isnan().all() and got[2][[1, 3]].isnan().all()
+    assert got[1][1].isnan() and got[1][3] == float("-inf")
