@@ -558,8 +558,9 @@ typedef struct sc_linear_desc {
  * significand) whose six leading products are summed in fp32.  bias, act and
  * residual are applied in fp32 and out is rounded once.  The tensor cores cut
  * sums where fp32 arithmetic rounds; where out is SC_F32, or a sum has more than
- * 16384 products, sums of at most 512 products are added up in fp32 arithmetic, so
- * that long ones do not drift (weight gradients likewise).
+ * 16384 products, sums of at most 768 products (512 with fp32 operands) are added
+ * up in fp32 arithmetic, so that long ones do not drift (weight gradients
+ * likewise).
  *   bias       (device, nullable) [N]
  *   residual   (device, nullable) [M][N] of out_type
  *   out        (device) out; may be residual itself (same stride)

@@ -183,6 +183,7 @@ int launch_gemm(int64_t M, int64_t N, int64_t K, int type16, const GemmOperand &
     // one accumulation, or chunks of it added in fp32
     const int sum = epi.out_type == SC_F32 ? SUM_F32 : p.n_k > LONG_16 ? SUM_16_LONG : SUM_16;
     p.chunk = sum == SUM_16 && sh.parts == 1 ? p.n_k : CHUNK;
+    p.lead = p.chunk == CHUNK && p.planes == 1 && p.n_k > 2 * CHUNK ? CHUNK_LEAD : p.chunk;
     // the two accumulators of fp32 operands: twice where two tiles' fit
     p.rest = p.planes == 1 ? 0 : sh.bn <= ACC_COLS / 2 ? ACC_COLS / 2 : ACC_COLS;
     p.acc_two = p.rest < ACC_COLS;

@@ -20,17 +20,17 @@
 // The tensor cores cut an fp32 sum where fp32 arithmetic rounds, so a long sum
 // drifts towards zero by about 2^-25 of itself per 16 indexes.  Where the
 // result keeps fp32, an accumulator therefore takes CHUNK steps at most, and
-// the epilogue warps add the chunks in registers.  (32896 x 1024 x 4096 with an
-// fp32 residual: off by 4.7e-7 of the result's norm in 239 us; 9.9e-7 in 228 with
-// chunks of 16, 4.0e-6 in one accumulation; a plain fp32 product is off by 6.1e-7.
-// 4112 x 4096 x 1024 takes 52 and 51, others alike: what costs time is that two
-// chunks of the next tile are all that runs under a tile's stores.)  A 16-bit result's rounding hides the
+// the epilogue warps add the chunks in registers.  The first two of a tile, all
+// that can run under the stores of the tile before, take CHUNK_LEAD where more
+// follow.  (32896 x 1024 x 4096 with an fp32 residual: off by 5.8e-7 of the
+// result's norm in 233 us; 4.7e-7 in 239 with 8 throughout, 9.9e-7 in 228 with 16,
+// 4.0e-6 in one accumulation; a plain fp32 product is off by 6.1e-7.)  A 16-bit result's rounding hides the
 // drift of LONG_16 steps (2^-15, half a step of fp16 is 2^-11); longer sums
 // are added up in chunks too (2048 x 2048 x 16384 in one accumulation 91.0 us,
 // 2048 x 2048 x 16448 in chunks 92.6).  fp32 operands keep the five small
 // products, below 2^-8 of the result, in an accumulator of their own, so that
-// only the leading product's drift counts (off by 4.7e-7 where chunks of 16 are
-// off by 1.0e-6; 4112 x 4096 x 1024 takes 157 us, 154 with 16; a plain fp32 product
+// only the leading product's drift counts, in chunks of CHUNK throughout (off by
+// 4.7e-7 where 16 are off by 1.0e-6; 4112 x 4096 x 1024 takes 157 us, 154 with 16; a plain fp32 product
 // is off by 5.7e-7).
 //
 // Kernels (one template):
@@ -76,6 +76,7 @@ constexpr int KEEP_REGS = 168;          // registers per thread of a kernel that
 constexpr int RING_BYTES = 160 * 1024;  // 5 stages of 32 KB
 constexpr int MAX_RING = 8;
 constexpr int CHUNK = 8;                // steps (512 indexes) per accumulation of an fp32 result
+constexpr int CHUNK_LEAD = 12;          // the first two of a tile of more, 16-bit operands
 constexpr int LONG_16 = 256;            // most steps of a 16-bit result in one accumulation
 // Epilogue staging, per warp: 32 rows x 64 columns of fp32, 16-byte quads
 // permuted so that both a lane's row (written) and 8 lanes' row (read) touch
@@ -101,7 +102,8 @@ struct GemmArgs {
     int M, N;
     int n_k;            // steps of 64 contraction indexes
     int planes;         // stages per step: 1, or 3 for fp32 operands
-    int chunk;          // steps per accumulation
+    int chunk;          // steps per accumulation,
+    int lead;           // of the first two of a tile
     int acc_two;        // 1: two accumulations fit tensor memory, 0: one
     int rest;           // columns from the leading parts' accumulator to the others', fp32 operands
     int a_mn, b_mn;     // operand has its own index contiguous
@@ -678,6 +680,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
         it0 = (int)((int64_t)p.n_k * rank / parts);
         it1 = (int)((int64_t)p.n_k * (rank + 1) / parts);
     }
+    // the end of the accumulation that begins at step i
+    auto chunk_end = [&](int i) { return min(i + (!SPLIT && i < 2 * p.lead ? p.lead : p.chunk), it1); };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < MAX_RING; ++s) {
@@ -845,7 +849,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
                 // add up the chunks: this lane's row, columns c_lo .. c_lo + half
                 constexpr int COLS = SPLIT ? SPLIT_N / 2 : GN_MAX / 2;
                 float v[COLS] = {};
-                for (int i = it0; i < it1; i += p.chunk, ++n) {
+                for (int i = it0; i < it1; i = chunk_end(i), ++n) {
                     const int buf = n & p.acc_two;
                     if (!wait(&sy.acc_full[buf], (n >> p.acc_two) & 1)) return;
                     tc_fence_after();
@@ -1052,7 +1056,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) gemm_kernel(const __grid_cons
                     }
                     tc_fence_after();
                     const uint32_t acc = tmem + buf * ACC_COLS;
-                    const int end = min(i + p.chunk, it1);
+                    const int end = chunk_end(i);
                     // the slot of the next stage, once it is there
                     auto arrived = [&](int &slot) {
                         if (!wait(&sy.full[r.slot], r.phase)) return ok = false;
