@@ -26,8 +26,8 @@
 // result's norm in 233 us; 4.7e-7 in 239 with 8 throughout, 9.9e-7 in 228 with 16,
 // 4.0e-6 in one accumulation; a plain fp32 product is off by 6.1e-7.)  A 16-bit result's rounding hides the
 // drift of LONG_16 steps (2^-15, half a step of fp16 is 2^-11); longer sums
-// are added up in chunks too (2048 x 2048 x 16384 in one accumulation 91.0 us,
-// 2048 x 2048 x 16448 in chunks 92.6).  fp32 operands keep the five small
+// are added up in chunks too (2048 x 2048 x 16384 in one accumulation 90.8 us,
+// 2048 x 2048 x 16448 in chunks 93.1).  fp32 operands keep the five small
 // products, below 2^-8 of the result, in an accumulator of their own, so that
 // only the leading product's drift counts, in chunks of CHUNK throughout (off by
 // 4.7e-7 where 16 are off by 1.0e-6; 4112 x 4096 x 1024 takes 157 us, 154 with 16; a plain fp32 product
@@ -45,12 +45,12 @@
 // an earlier pass if the caller has any, warps 4 to 11 are the epilogue.
 //
 // Measured (us, one B200, a replayed graph over two or three sets of inputs after a
-// second's rest): 8192^3 bf16 690 (cuBLAS 654); 4112 x 4096 x 1024 30 plain
-// (cuBLAS 29), 40 with gelu and the pre-activation kept, where the epilogue sets
-// the pace (tensor pipe 51 % busy); 32896 x 1024 x 4096 178 (cuBLAS 179), 211 with
-// an fp32 residual and result (tensor pipe 77 %).  Products that run for longer
-// meet the power limit: the last one takes 247 us replayed and 259 called for 1.5 s,
-// at 1180 and 1120 MHz.
+// second's rest): 8192^3 bf16 694 (cuBLAS 657); 4112 x 4096 x 1024 30 plain
+// (cuBLAS 30), 40 with gelu and the pre-activation kept, where the epilogue sets
+// the pace (tensor pipe 51 % busy); 32896 x 1024 x 4096 179 (cuBLAS 181), 197 with
+// an fp32 result, 220 with a residual beside it (tensor pipe 74 %).  Products that
+// run for longer meet the power limit: the last one takes 266 us replayed and 272
+// called for 1.5 s, at 1250 and 1240 MHz.
 // All waits are bounded, as in the count engine.  A CTA (a pair, a cluster that
 // shares a tile) whose wait expires waits for its own copies and products,
 // writes NaN over its tiles, records SC_DEV_WAIT_LIMIT, frees tensor memory and
